@@ -447,6 +447,108 @@ fa_status_t noalloc_scratch(void** out) {
   return FA_OK;
 }
 
+// ------------------------------------------------------------------------------------
+// Per-head norm and rotary positions
+// ------------------------------------------------------------------------------------
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// One kind of rows on one side of the call. Null or no heads: absent (*out has heads 0).
+// Vectors of 16 bytes are loaded and stored, so strides are multiples of 8 elements; rows
+// that are written must not overlap one another (*written).
+fa_status_t resolve_rows(const fa_heads_t* h, int B, int N, int d, bool packed, bool written,
+                         fa::HeadRows* out) {
+  *out = fa::HeadRows{nullptr, 0, 0, 0, 0};
+  if (h == nullptr || h->heads == 0) return FA_OK;
+  if (h->heads < 0 || h->data == nullptr) return FA_ERR_INVALID_ARG;
+  if ((packed ? (long long)N : (long long)B * N) * h->heads * d >= (1ll << 31))
+    return FA_ERR_UNSUPPORTED;
+  // (stride, extent) of each dimension, the smallest stride first
+  struct Dim {
+    long long stride;
+    int extent;
+  } dims[3] = {{h->head_stride, h->heads},
+               {h->token_stride, N},
+               {packed ? 0 : h->batch_stride, packed ? 1 : B}};
+  for (Dim& x : dims)
+    if (x.extent <= 1) x = Dim{0, 1};  // never stepped: its stride does not matter
+  for (const Dim& x : dims) {
+    if (x.stride < 0 || x.stride >= (1ll << 40)) return FA_ERR_INVALID_ARG;
+    if (x.stride % 8 != 0) return FA_ERR_MISALIGNED;
+  }
+  if (!aligned16(h->data)) return FA_ERR_MISALIGNED;
+  if (written) {
+    for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < 2 - i; ++j)
+        if (dims[j].stride > dims[j + 1].stride) std::swap(dims[j], dims[j + 1]);
+    long long span = d;
+    for (const Dim& x : dims) {
+      if (x.extent <= 1) continue;
+      if (x.stride < span) return FA_ERR_INVALID_ARG;
+      span += (x.extent - 1) * x.stride;
+    }
+  }
+  *out = fa::HeadRows{static_cast<__nv_bfloat16*>(h->data), h->heads,
+                      packed ? 0 : h->batch_stride, h->token_stride, h->head_stride};
+  return FA_OK;
+}
+
+// Checks the parameters both directions share and fills `a` with them; *tokens: of the call.
+fa_status_t resolve_rope(int B, int N, int d, const fa_norm_rope_t* p, fa::RopeArgs* a) {
+  *a = fa::RopeArgs();
+  if (p == nullptr || B < 0 || N < 0) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  const bool packed = p->cu_seqlens != nullptr;
+  if (packed && (p->seq_lengths != nullptr || p->total_tokens < 0)) return FA_ERR_INVALID_ARG;
+  if (!packed && (long long)B * N >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  if (p->norm) {
+    if (!std::isfinite(p->eps) || !(p->eps >= 0.f)) return FA_ERR_INVALID_ARG;
+  } else if (p->q_weight != nullptr || p->k_weight != nullptr) {
+    return FA_ERR_INVALID_ARG;
+  }
+  if (p->rotary_dim < 0) return FA_ERR_INVALID_ARG;
+  if (p->rotary_dim > d || p->rotary_dim % 16 != 0) return FA_ERR_UNSUPPORTED;
+  if (p->rotary_dim > 0) {
+    if (p->inv_freq == nullptr || p->axes < 1) return FA_ERR_INVALID_ARG;
+    if (p->axes > FA_MAX_AXES) return FA_ERR_UNSUPPORTED;
+    if (p->axes > 1 && (p->positions == nullptr || p->pair_axis == nullptr))
+      return FA_ERR_INVALID_ARG;
+    a->rot = p->rotary_dim;
+    a->axes = p->axes;
+    a->inv_freq = p->inv_freq;
+    a->pair_axis = p->pair_axis;
+    a->positions = p->positions;
+  }
+  for (const void* x : {(const void*)p->q_weight, (const void*)p->k_weight,
+                        (const void*)a->inv_freq, (const void*)a->positions,
+                        (const void*)p->seq_lengths, (const void*)p->cu_seqlens})
+    if (!aligned4(x)) return FA_ERR_MISALIGNED;
+  a->norm = p->norm ? 1 : 0;
+  a->eps = p->eps;
+  a->w[0] = p->q_weight;
+  a->w[1] = p->k_weight;
+  a->seq_len = p->seq_lengths;
+  a->cu = p->cu_seqlens;
+  a->B = B;
+  a->N = N;
+  a->tokens = packed ? (B == 0 || N == 0 ? 0 : p->total_tokens) : B * N;
+  return FA_OK;
+}
+
+fa_status_t resolve_sides(const fa_heads_t* const (&in)[3], const fa_heads_t* const (&out)[3],
+                          bool in_given, int d, bool packed, const fa::RopeArgs& a,
+                          fa::HeadRows (&x)[3], fa::HeadRows (&y)[3], bool x_written,
+                          bool y_written) {
+  const int N = packed ? a.tokens : a.N;
+  for (int i = 0; i < 3; ++i) {
+    fa_status_t s;
+    if ((s = resolve_rows(out[i], a.B, N, d, packed, y_written, &y[i])) != FA_OK) return s;
+    if (!in_given) continue;
+    if ((s = resolve_rows(in[i], a.B, N, d, packed, x_written, &x[i])) != FA_OK) return s;
+    if (x[i].heads != y[i].heads) return FA_ERR_INVALID_ARG;
+  }
+  return FA_OK;
+}
+
 }  // namespace
 
 // The library is compiled with hidden visibility: only the entry points of include/fa.h
@@ -621,6 +723,65 @@ fa_status_t fa_bwd_noalloc(const void* q, const void* k, const void* v, const vo
                   scratch, stream);
 }
 
+fa_status_t fa_qk_norm_rope_fwd(const fa_heads_t* q, const fa_heads_t* k, const fa_heads_t* v,
+                                const fa_heads_t* q_out, const fa_heads_t* k_out,
+                                const fa_heads_t* v_out, int B, int N, int d,
+                                const fa_norm_rope_t* params, void* stream) {
+  fa::RopeArgs a;
+  fa_status_t s = resolve_rope(B, N, d, params, &a);
+  if (s != FA_OK || a.tokens == 0) return s;
+  if ((s = resolve_sides({q, k, v}, {q_out, k_out, v_out}, true, d, a.cu != nullptr, a, a.x, a.y,
+                         false, true)) != FA_OK)
+    return s;
+  if (a.y[0].heads + a.y[1].heads + a.y[2].heads == 0) return FA_OK;
+  return fa_host::launch_rope_fwd(a, d, params->interleaved != 0,
+                                  static_cast<cudaStream_t>(stream));
+}
+
+size_t fa_qk_norm_rope_workspace_bytes(int d) {
+  if (d != 64 && d != 128) return 0;
+  return (size_t)fa::kRopeMaxBlocks * 2 * d * sizeof(float);
+}
+
+fa_status_t fa_qk_norm_rope_bwd(const fa_heads_t* dq, const fa_heads_t* dk, const fa_heads_t* dv,
+                                const fa_heads_t* q, const fa_heads_t* k,
+                                const fa_heads_t* gq, const fa_heads_t* gk, const fa_heads_t* gv,
+                                float* gq_weight, float* gk_weight, int B, int N, int d,
+                                const fa_norm_rope_t* params, void* workspace,
+                                size_t workspace_bytes_given, void* stream) {
+  fa::RopeArgs a;
+  fa_status_t s = resolve_rope(B, N, d, params, &a);
+  if (s != FA_OK) return s;
+  const bool gains = gq_weight != nullptr || gk_weight != nullptr;
+  if (gains && !a.norm) return FA_ERR_INVALID_ARG;
+  if (!aligned4(gq_weight) || !aligned4(gk_weight)) return FA_ERR_MISALIGNED;
+  if (gains) {
+    if ((s = check_ptrs({workspace})) != FA_OK) return s;
+    if (workspace_bytes_given < fa_qk_norm_rope_workspace_bytes(d)) return FA_ERR_WORKSPACE;
+  }
+  if (a.tokens > 0) {
+    fa::HeadRows in[3] = {};
+    const bool packed = a.cu != nullptr;
+    // the incoming gradients against the projection's, then the projection's rows (needed
+    // for the norm alone)
+    if ((s = resolve_sides({gq, gk, gv}, {dq, dk, dv}, true, d, packed, a, a.g, a.y, true,
+                           false)) != FA_OK)
+      return s;
+    if (a.norm) {
+      if ((s = resolve_sides({q, k, gv}, {dq, dk, dv}, true, d, packed, a, a.x, in, false,
+                             false)) != FA_OK)
+        return s;
+    }
+  }
+  if (a.y[0].heads + a.y[1].heads + a.y[2].heads == 0) a.tokens = 0;
+  if (a.tokens == 0 && !gains) return FA_OK;
+  a.partial = gains ? static_cast<float*>(workspace) : nullptr;
+  a.dw[0] = gq_weight;
+  a.dw[1] = gk_weight;
+  return fa_host::launch_rope_bwd(a, d, params->interleaved != 0,
+                                  static_cast<cudaStream_t>(stream));
+}
+
 const char* fa_status_string(fa_status_t status) {
   switch (status) {
     case FA_OK: return "FA_OK";
@@ -656,7 +817,7 @@ fa_status_t fa_debug_set_fault(int fault) {
   return FA_OK;
 }
 
-int fa_version(void) { return 200; }
+int fa_version(void) { return 300; }
 
 }  // extern "C"
 #pragma GCC visibility pop

@@ -10,6 +10,7 @@
 
 #include "fa.h"
 #include "rng.cuh"
+#include "rope_args.h"
 #include "tiles.cuh"
 
 namespace fa_host {
@@ -87,6 +88,11 @@ fa_status_t launch_dq(const void* q, const void* k, const void* v, const void* d
 template <int D>
 fa_status_t launch_fill_past_length(void* t0, void* t1, void* t2, float* lse,
                                     const int* seq_len, int BH, int H, int N, cudaStream_t st);
+
+// Per-head norm and rotary positions (fa_rope.cuh); the backward also writes a.dw when
+// a.partial is given (a call of no tokens: zeros). a.splits is set here.
+fa_status_t launch_rope_fwd(const fa::RopeArgs& a, int d, bool interleaved, cudaStream_t st);
+fa_status_t launch_rope_bwd(const fa::RopeArgs& a, int d, bool interleaved, cudaStream_t st);
 
 // Reads and clears the device status word of each kernel unit (0 = nothing recorded);
 // returns -1 if reading it failed.

@@ -8,6 +8,7 @@ library's kernels; if the library cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -26,7 +27,8 @@ STATUS_NAMES = {
 EXPORTED = ("fa_fwd", "fa_fwd_ex", "fa_fwd_fp8", "fa_bwd_workspace_bytes",
             "fa_bwd_workspace_bytes_ex", "fa_bwd", "fa_bwd_ex",
             "fa_fwd_alibi", "fa_bwd_alibi", "fa_bwd_preprocess", "fa_bwd_dkdv", "fa_bwd_dq",
-            "fa_bwd_fused", "fa_bwd_dq_convert", "fa_bwd_noalloc", "fa_status_string",
+            "fa_bwd_fused", "fa_bwd_dq_convert", "fa_bwd_noalloc", "fa_qk_norm_rope_fwd",
+            "fa_qk_norm_rope_workspace_bytes", "fa_qk_norm_rope_bwd", "fa_status_string",
             "fa_debug_status", "fa_debug_set_fault", "fa_version")
 
 #: fa_options_t.flags: the fused backward (head_dim 64; dQ by fp32 reductions)
@@ -51,6 +53,23 @@ class fa_options_t(ctypes.Structure):
                 ("flags", ctypes.c_uint), ("dropout_seed", ctypes.c_ulonglong),
                 ("dropout_offset", ctypes.c_ulonglong), ("seq_lengths", ctypes.c_void_p),
                 ("cu_seqlens", ctypes.c_void_p), ("total_tokens", ctypes.c_int)]
+
+
+class fa_heads_t(ctypes.Structure):
+    """Rows of queries, keys or values with their strides (include/fa.h)."""
+    _fields_ = [("data", ctypes.c_void_p), ("heads", ctypes.c_int),
+                ("batch_stride", ctypes.c_longlong), ("token_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong)]
+
+
+class fa_norm_rope_t(ctypes.Structure):
+    """Parameters of fa_qk_norm_rope_fwd and _bwd (include/fa.h)."""
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p), ("pair_axis", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("seq_lengths", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("norm", ctypes.c_int), ("rotary_dim", ctypes.c_int), ("axes", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("total_tokens", ctypes.c_int)]
 
 
 def options(alibi_slopes=None, key_padding=None, o_low=None, dropout_p=0.0, dropout_seed=0,
@@ -100,6 +119,12 @@ def _lib() -> ctypes.CDLL:
         lib.fa_bwd_dq_convert.argtypes = [vp, vp, I, I, I, I, F, vp]
         lib.fa_bwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, I, I, I, I, F, I, W,
                                        vp]
+        HP, NP = ctypes.POINTER(fa_heads_t), ctypes.POINTER(fa_norm_rope_t)
+        lib.fa_qk_norm_rope_fwd.argtypes = [HP, HP, HP, HP, HP, HP, I, I, I, NP, vp]
+        lib.fa_qk_norm_rope_bwd.argtypes = [HP, HP, HP, HP, HP, HP, HP, HP, vp, vp, I, I, I, NP,
+                                            vp, ctypes.c_size_t, vp]
+        lib.fa_qk_norm_rope_workspace_bytes.argtypes = [I]
+        lib.fa_qk_norm_rope_workspace_bytes.restype = ctypes.c_size_t
         lib.fa_status_string.argtypes = [I]
         lib.fa_status_string.restype = ctypes.c_char_p
         lib.fa_debug_status.argtypes = [vp]
@@ -107,8 +132,9 @@ def _lib() -> ctypes.CDLL:
         lib.fa_version.argtypes = []
         for name in ("fa_fwd", "fa_fwd_ex", "fa_fwd_fp8", "fa_bwd", "fa_bwd_ex", "fa_fwd_alibi",
                      "fa_bwd_alibi", "fa_bwd_preprocess", "fa_bwd_fused", "fa_bwd_dq_convert",
-                     "fa_bwd_dkdv", "fa_bwd_dq", "fa_bwd_noalloc", "fa_debug_status",
-                     "fa_debug_set_fault", "fa_version"):
+                     "fa_bwd_dkdv", "fa_bwd_dq", "fa_bwd_noalloc", "fa_qk_norm_rope_fwd",
+                     "fa_qk_norm_rope_bwd", "fa_debug_status", "fa_debug_set_fault",
+                     "fa_version"):
             getattr(lib, name).restype = I
         _LIB = lib
     return _LIB
@@ -314,6 +340,24 @@ def fa_bwd_noalloc(q, k, v, o, do, lse, dq, dk, dv, scale=None, causal=False, wi
                                  _stream(stream)), "fa_bwd_noalloc")
 
 
+def fa_qk_norm_rope_fwd(q, k, v, q_out, k_out, v_out, B, N, d, params, stream=None) -> None:
+    """q .. v_out: fa_heads_t or None; params: fa_norm_rope_t."""
+    _check(_lib().fa_qk_norm_rope_fwd(q, k, v, q_out, k_out, v_out, B, N, d, params,
+                                      _stream(stream)), "fa_qk_norm_rope_fwd")
+
+
+def fa_qk_norm_rope_workspace_bytes(d: int) -> int:
+    return int(_lib().fa_qk_norm_rope_workspace_bytes(d))
+
+
+def fa_qk_norm_rope_bwd(dq, dk, dv, q, k, gq, gk, gv, gq_weight, gk_weight, B, N, d, params,
+                        workspace=None, stream=None) -> None:
+    """dq .. gv: fa_heads_t or None; gq_weight, gk_weight: fp32 tensors or None."""
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib().fa_qk_norm_rope_bwd(dq, dk, dv, q, k, gq, gk, gv, _ptr(gq_weight),
+                                      _ptr(gk_weight), B, N, d, params, _ptr(workspace), nbytes,
+                                      _stream(stream)), "fa_qk_norm_rope_bwd")
+
 
 def fa_status_string(status: int) -> str:
     return _lib().fa_status_string(int(status)).decode()
@@ -461,3 +505,204 @@ def attention_backward(q, k, v, o, lse, do, scale=None, causal=False, window=(-1
         fa_bwd_ex(q, k, v, o, do, lse, dq, dk, dv, ws, opt, scale, causal, window, stream,
                   dims=(B, H, N, d))
     return dq, dk, dv
+
+
+# ------------------------------------------------- per-head norm and rotary positions
+def _check_rows(t, name, like, tokens, d):
+    """A bf16 CUDA tensor of (tokens..., heads, d) rows on `like`'s device, d consecutive."""
+    if t.dtype != torch.bfloat16 or t.device != like.device or not t.is_cuda:
+        raise ValueError("%s must be a bf16 tensor on the queries' CUDA device" % name)
+    if t.dim() != len(tokens) + 2 or tuple(t.shape[:-2]) != tokens or t.shape[-1] != d:
+        raise ValueError("%s must have the queries' tokens and head_dim" % name)
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError("%s must hold each head's values consecutively" % name)
+
+
+def _projection_rows(t):
+    """The fa_heads_t of a (B, N, H, d) or packed (total, H, d) tensor of any strides."""
+    if t is None:
+        return None
+    st = t.stride()
+    if len(st) == 4:
+        return fa_heads_t(t.data_ptr(), t.shape[2], st[0], st[1], st[2])
+    return fa_heads_t(t.data_ptr(), t.shape[1], 0, st[0], st[1])
+
+
+def _attention_rows(t):
+    """The fa_heads_t of a (B, H, N, d) or packed (total, H, d) tensor."""
+    if t is None:
+        return None
+    st = t.stride()
+    if len(st) == 4:
+        return fa_heads_t(t.data_ptr(), t.shape[1], st[0], st[2], st[1])
+    return fa_heads_t(t.data_ptr(), t.shape[1], 0, st[0], st[1])
+
+
+def _check_aux(t, name, dtype, like, shape):
+    if t.dtype != dtype or t.device != like.device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor on the queries' device"
+                         % (name, str(dtype).replace("torch.", "")))
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s" % (name, shape))
+
+
+def _norm_rope_params(like, tokens, d, q_weight, k_weight, eps, norm, inv_freq, positions,
+                      pair_axis, interleaved, seq_lengths, cu_seqlens, max_seqlen):
+    """(B, N, fa_norm_rope_t) of a call on (tokens..., H, d) rows."""
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            if not norm:
+                raise ValueError("%s is a gain of the norm" % name)
+            _check_aux(w, name, torch.float32, like, (d,))
+    rot, axes = 0, 1
+    if inv_freq is not None:
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must hold one frequency per rotation")
+        _check_aux(inv_freq, "inv_freq", torch.float32, like, (inv_freq.numel(),))
+        rot = 2 * inv_freq.numel()
+        if positions is not None:
+            if positions.dim() == len(tokens) + 1:
+                axes = positions.shape[0]
+                _check_aux(positions, "positions", torch.int32, like, (axes,) + tokens)
+            else:
+                _check_aux(positions, "positions", torch.int32, like, tokens)
+        if pair_axis is not None:
+            _check_aux(pair_axis, "pair_axis", torch.uint8, like, (rot // 2,))
+    elif positions is not None or pair_axis is not None:
+        raise ValueError("positions and pair_axis need inv_freq")
+    total = 0
+    if cu_seqlens is not None:
+        if seq_lengths is not None:
+            raise ValueError("seq_lengths and cu_seqlens exclude each other")
+        if len(tokens) != 1:
+            raise ValueError("a packed batch takes (total_tokens, heads, head_dim) tensors")
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must hold B + 1 >= 2 offsets")
+        _check_aux(cu_seqlens, "cu_seqlens", torch.int32, like, (cu_seqlens.numel(),))
+        if max_seqlen is None or int(max_seqlen) < 1:
+            raise ValueError("a packed batch needs max_seqlen >= 1 (the longest sequence)")
+        B, N, total = cu_seqlens.numel() - 1, int(max_seqlen), tokens[0]
+    else:
+        if len(tokens) != 2:
+            raise ValueError("(total_tokens, heads, head_dim) tensors need cu_seqlens")
+        B, N = tokens
+        if seq_lengths is not None:
+            _check_aux(seq_lengths, "seq_lengths", torch.int32, like, (B,))
+    return B, N, fa_norm_rope_t(_ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(pair_axis),
+                                _ptr(positions), _ptr(seq_lengths), _ptr(cu_seqlens), eps,
+                                1 if norm else 0, rot, axes, 1 if interleaved else 0, total)
+
+
+def _on_device(fn):
+    """Runs a call on the device its first tensor is on, whichever device is current."""
+    @functools.wraps(fn)
+    def call(t, *args, **kw):
+        if t.is_cuda and t.device.index != torch.cuda.current_device():
+            with torch.cuda.device(t.device):
+                return fn(t, *args, **kw)
+        return fn(t, *args, **kw)
+    return call
+
+
+def _scratch(nbytes, device, stream):
+    """A workspace that stays out of the allocator's hands until `stream` (None: the current
+    one) has passed the kernels launched on it."""
+    ws = torch.empty(max(1, nbytes), dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(torch.cuda.ExternalStream(_stream(stream), device=device))
+    return ws
+
+
+@_on_device
+def qk_norm_rope_forward(q, k, v=None, q_weight=None, k_weight=None, eps=1e-6, norm=True,
+                         inv_freq=None, positions=None, pair_axis=None, interleaved=False,
+                         seq_lengths=None, cu_seqlens=None, max_seqlen=None, stream=None):
+    """Queries and keys normalised per head and rotated by their positions, with the values, in
+    the layout attention_forward takes. q, k, v: bf16 CUDA tensors (B, N, heads, d) of any token
+    and head strides (views of a fused projection), d 64 or 128; returns contiguous
+    (B, heads, N, d) tensors (Q, K), or (Q, K, V) with v. A packed batch (cu_seqlens with
+    max_seqlen, as in attention_forward) takes and returns (total, heads, d).
+    norm: each row divided by sqrt(mean of squares + eps), times the gain q_weight / k_weight
+    (d fp32 values; None = ones). inv_freq (rotary_dim / 2 fp32): rotation p turns values
+    (p, p + rotary_dim / 2), or (2p, 2p + 1) when interleaved, by position * inv_freq[p]; None =
+    no rotation. positions ((B, N) or (total,) int32; None = the place in the sequence): with
+    several axes (axes, B, N) or (axes, total), and pair_axis (rotary_dim / 2 uint8) names each
+    rotation's axis. seq_lengths ((B,) int32): rows past a length are zero."""
+    tokens, d = tuple(q.shape[:-2]), q.shape[-1]
+    _check_rows(q, "q", q, tokens, d)
+    _check_rows(k, "k", q, tokens, d)
+    if v is not None:
+        _check_rows(v, "v", q, tokens, d)
+    B, N, params = _norm_rope_params(q, tokens, d, q_weight, k_weight, eps, norm, inv_freq,
+                                     positions, pair_axis, interleaved, seq_lengths, cu_seqlens,
+                                     max_seqlen)
+    outs = []
+    for t in (q, k, v):
+        if t is None:
+            outs.append(None)
+        elif len(tokens) == 2:
+            outs.append(torch.empty((B, t.shape[2], N, d), dtype=t.dtype, device=t.device))
+        else:
+            outs.append(torch.empty((tokens[0], t.shape[1], d), dtype=t.dtype, device=t.device))
+    fa_qk_norm_rope_fwd(_projection_rows(q), _projection_rows(k), _projection_rows(v),
+                        _attention_rows(outs[0]), _attention_rows(outs[1]),
+                        _attention_rows(outs[2]), B, N, d, params, stream)
+    return tuple(outs) if v is not None else tuple(outs[:2])
+
+
+@_on_device
+def qk_norm_rope_backward(dq, dk, dv=None, q=None, k=None, q_weight=None, k_weight=None, eps=1e-6,
+                          norm=True, inv_freq=None, positions=None, pair_axis=None,
+                          interleaved=False, seq_lengths=None, cu_seqlens=None, max_seqlen=None,
+                          stream=None, out=None):
+    """The gradient of qk_norm_rope_forward from those of its outputs, (B, heads, N, d) or packed
+    (total, heads, d) (as attention_backward returns them): (gq, gk, gv, gq_weight, gk_weight),
+    gv None without dv, the gains' None for a gain that is None. q, k: the forward's inputs
+    (needed with norm). out: three tensors (the third None without dv) of the forward's input
+    shapes, of any strides that do not overlap, to write gq, gk, gv to; by default they are views
+    of one new (B, N, heads of all, d) or (total, heads of all, d) tensor."""
+    if dq.dim() not in (3, 4):
+        raise ValueError("dq must be (B, heads, N, d) or packed (total, heads, d)")
+    packed = dq.dim() == 3
+    # token-major views
+    dqt, dkt, dvt = (t if t is None or packed or t.dim() != 4 else t.transpose(1, 2)
+                     for t in (dq, dk, dv))
+    tokens, d = tuple(dqt.shape[:-2]), dqt.shape[-1]
+    grads = (("dq", dqt), ("dk", dkt)) + ((("dv", dvt),) if dv is not None else ())
+    for name, t in grads:
+        _check_rows(t, name, dq, tokens, d)
+    if norm:
+        if q is None or k is None:
+            raise ValueError("the norm's gradient needs q and k")
+        for name, t, g in (("q", q, dqt), ("k", k, dkt)):
+            _check_rows(t, name, dq, tokens, d)
+            if t.shape != g.shape:
+                raise ValueError("%s must have its gradient's heads" % name)
+    B, N, params = _norm_rope_params(dq, tokens, d, q_weight, k_weight, eps, norm, inv_freq,
+                                     positions, pair_axis, interleaved, seq_lengths, cu_seqlens,
+                                     max_seqlen)
+    if out is None:
+        heads = [t.shape[-2] for _, t in grads]
+        out = list(torch.empty(tokens + (sum(heads), d), dtype=dq.dtype, device=dq.device)
+                   .split(heads, -2))
+    else:
+        out = [t for t in out if t is not None]
+        if len(out) != len(grads):
+            raise ValueError("out must hold one tensor per gradient")
+        for t, (name, g) in zip(out, grads):
+            _check_rows(t, "out", dq, tokens, d)
+            if t.shape != g.shape:
+                raise ValueError("out must have the shapes of the forward's inputs")
+    if dv is None:
+        out.append(None)
+    gqw = torch.empty_like(q_weight) if q_weight is not None else None
+    gkw = torch.empty_like(k_weight) if k_weight is not None else None
+    ws = None
+    if gqw is not None or gkw is not None:
+        ws = _scratch(fa_qk_norm_rope_workspace_bytes(d), dq.device, stream)
+    fa_qk_norm_rope_bwd(_projection_rows(dqt), _projection_rows(dkt), _projection_rows(dvt),
+                        _projection_rows(q) if norm else None,
+                        _projection_rows(k) if norm else None,
+                        _projection_rows(out[0]), _projection_rows(out[1]),
+                        _projection_rows(out[2]), gqw, gkw, B, N, d, params, ws, stream)
+    return out[0], out[1], out[2], gqw, gkw

@@ -356,6 +356,105 @@ fa_status_t fa_bwd_noalloc(const void *q, const void *k, const void *v, const vo
                            int B, int H, int N, int d, float scale, int causal,
                            fa_window_t window, void *stream);
 
+/*
+ * Per-head norm and rotary positions: from a projection's output to the queries, keys and
+ * values of the attention above, and back. (The pages have no counterpart; it is an interface
+ * addition of this library.) For a row x of a query or key head, with the head kind's gain w and
+ * the token's position on each axis,
+ *
+ *     x^ = x / sqrt(mean(x^2) + eps)          (norm != 0; else x^ = x)
+ *     y  = R (w o x^)
+ *
+ * where R turns the pair of values of rotation p = 0 .. rotary_dim/2 - 1 by the angle
+ * positions[pair_axis[p]] * inv_freq[p]: (y_e, y_f) = (e cos - f sin, f cos + e sin). The pair
+ * of rotation p is values (2p, 2p + 1) with interleaved != 0, else values
+ * (p, p + rotary_dim/2); values from rotary_dim on are not turned. Value rows are carried
+ * along unchanged, so that one call turns views of a fused projection into the attention's
+ * tensors. Everything is computed in fp32 (angles exactly reduced, so that positions may be any
+ * int32, also negative) and rounded once to bf16.
+ *
+ * fa_heads_t: the rows of one kind (queries, keys or values). Row h of token n of batch entry b
+ * holds d consecutive bf16 values at data + b batch_stride + n token_stride + h head_stride
+ * (strides in elements, multiples of 8 (FA_ERR_MISALIGNED), in [0, 2^40); a stride that is never
+ * stepped is not looked at); data is 16-byte aligned. Rows that are read may overlap (stride 0:
+ * shared rows); rows that are written must not (FA_ERR_INVALID_ARG), and may be the call's own
+ * input rows, at the same address and strides. In a packed batch there is no batch dimension
+ * and token n is the n-th of the tensor. A null pointer or heads = 0 means none of that kind;
+ * both sides of a call have the same heads of each kind (FA_ERR_INVALID_ARG). Heads need not be
+ * the same for queries, keys and values. B N heads d (packed: total_tokens heads d) must be
+ * below 2^31 (FA_ERR_UNSUPPORTED).
+ */
+typedef struct {
+    void *data;
+    int heads;
+    long long batch_stride;
+    long long token_stride;
+    long long head_stride;
+} fa_heads_t;
+
+/*
+ * Parameters of a call, the same for the forward and the backward. Device pointers, 4-byte
+ * aligned (pair_axis: any alignment).
+ *   q_weight, k_weight  d fp32 gains, or NULL for ones; only with norm (FA_ERR_INVALID_ARG).
+ *   inv_freq    rotary_dim/2 fp32 angles per position, finite; NULL only if rotary_dim is 0.
+ *   pair_axis   rotary_dim/2 bytes, the axis of each rotation (values of axes and above count
+ *               as axes - 1), or NULL if there is one axis.
+ *   positions   (axes, B, N) int32, packed (axes, total_tokens); or NULL with one axis: each
+ *               token's place in its sequence.
+ *   seq_lengths B int32 real lengths of a padded batch, or NULL: rows past a length are not
+ *               read, get zeros, and add nothing to the gains' gradients.
+ *   cu_seqlens, total_tokens
+ *               a packed batch as in fa_options_t, or NULL / 0; offsets must not decrease. N is
+ *               the longest sequence handled. Tokens that no sequence covers (before the first,
+ *               behind the last, past N) are neither read nor written. Exclusive with
+ *               seq_lengths (FA_ERR_INVALID_ARG).
+ *   eps         finite, >= 0.
+ *   rotary_dim  a multiple of 16 in [0, d] (else FA_ERR_UNSUPPORTED); 0: no rotation.
+ *   axes        1 .. FA_MAX_AXES (above: FA_ERR_UNSUPPORTED); not looked at without rotation.
+ */
+#define FA_MAX_AXES 3
+
+typedef struct {
+    const float *q_weight;
+    const float *k_weight;
+    const float *inv_freq;
+    const unsigned char *pair_axis;
+    const int *positions;
+    const int *seq_lengths;
+    const int *cu_seqlens;
+    float eps;
+    int norm;
+    int rotary_dim;
+    int axes;
+    int interleaved;
+    int total_tokens;
+} fa_norm_rope_t;
+
+/* q_out, k_out, v_out from q, k, v (v and v_out may be NULL: queries and keys alone). */
+fa_status_t fa_qk_norm_rope_fwd(const fa_heads_t *q, const fa_heads_t *k, const fa_heads_t *v,
+                                const fa_heads_t *q_out, const fa_heads_t *k_out,
+                                const fa_heads_t *v_out, int B, int N, int d,
+                                const fa_norm_rope_t *params, void *stream);
+
+/* Bytes of workspace fa_qk_norm_rope_bwd needs when a gain's gradient is asked for; 0 for an
+ * unsupported d. */
+size_t fa_qk_norm_rope_workspace_bytes(int d);
+
+/*
+ * The gradient: gq, gk, gv (bf16) from the gradients dq, dk, dv of the forward's outputs and,
+ * with norm, the forward's inputs q, k (not looked at without it). gq_weight, gk_weight: d fp32
+ * sums over all rows, or NULL (a call of no tokens writes zeros); they need norm
+ * (FA_ERR_INVALID_ARG) and a workspace, 16-byte aligned, of fa_qk_norm_rope_workspace_bytes(d)
+ * bytes (FA_ERR_WORKSPACE), which calls that overlap on the GPU must not share. Results are
+ * bit-identical from run to run.
+ */
+fa_status_t fa_qk_norm_rope_bwd(const fa_heads_t *dq, const fa_heads_t *dk, const fa_heads_t *dv,
+                                const fa_heads_t *q, const fa_heads_t *k,
+                                const fa_heads_t *gq, const fa_heads_t *gk, const fa_heads_t *gv,
+                                float *gq_weight, float *gk_weight, int B, int N, int d,
+                                const fa_norm_rope_t *params, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char *fa_status_string(fa_status_t status);
 
