@@ -74,17 +74,25 @@ fa_status_t dispatch_features(std::integer_sequence<int, Fs...>, int feat, Args&
 }
 
 // forward: every combination of ALiBi, key padding, residual and dropout, in the (B, H, N, d)
-// layout and packed (kFeatPacked = 32); at head_dim 128 also the e4m3 forward
+// layout and packed (kFeatPacked = 32), each also with capped scores or a prefix
+// (kFeatScore = 64); at head_dim 128 also the e4m3 forward
 using FwdFeatures64 = std::integer_sequence<int, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14,
                                             15, 32, 33, 34, 35, 36, 37, 38, 39, 40, 41, 42, 43,
-                                            44, 45, 46, 47>;
+                                            44, 45, 46, 47, 64, 65, 66, 67, 68, 69, 70, 71, 72,
+                                            73, 74, 75, 76, 77, 78, 79, 96, 97, 98, 99, 100, 101,
+                                            102, 103, 104, 105, 106, 107, 108, 109, 110, 111>;
 using FwdFeatures128 = std::integer_sequence<int, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13,
                                              14, 15, 16, 32, 33, 34, 35, 36, 37, 38, 39, 40, 41,
-                                             42, 43, 44, 45, 46, 47>;
+                                             42, 43, 44, 45, 46, 47, 64, 65, 66, 67, 68, 69, 70,
+                                             71, 72, 73, 74, 75, 76, 77, 78, 79, 96, 97, 98, 99,
+                                             100, 101, 102, 103, 104, 105, 106, 107, 108, 109,
+                                             110, 111>;
 // backward passes: ALiBi, key padding and dropout (the residual only changes delta), in both
-// layouts; the fused pass only in the (B, H, N, d) layout
+// layouts, with and without kFeatScore; the fused pass only in the (B, H, N, d) layout and
+// without kFeatScore
 using BwdFeatures = std::integer_sequence<int, 0, 1, 2, 3, 8, 9, 10, 11, 32, 33, 34, 35, 40, 41,
-                                          42, 43>;
+                                          42, 43, 64, 65, 66, 67, 72, 73, 74, 75, 96, 97, 98, 99,
+                                          104, 105, 106, 107>;
 using FusedFeatures = std::integer_sequence<int, 0, 1, 2, 3, 8, 9, 10, 11>;
 
 // The launchers as class templates over the feature flags, for dispatch_features.
@@ -202,6 +210,31 @@ fa_status_t resolve_options(const fa_options_t* opt, Extras* x) {
     x->drop.threshold = (uint32_t)t;
     x->drop.keep_scale = (float)(256.0 / (256.0 - t));
   }
+  return FA_OK;
+}
+
+// The cap and the prefixes of a _score call, checked and added to x. A prefix is for causal
+// problems without a left window. The cap's factors (scale / c, its inverse, c log2 e) have to
+// be ordinary fp32 numbers.
+fa_status_t resolve_score(const fa_score_t* score, float scale, int causal, fa_window_t window,
+                          Extras* x) {
+  if (score == nullptr) return FA_OK;
+  const float c = score->softcap;
+  if (!std::isfinite(c) || c < 0.f) return FA_ERR_INVALID_ARG;
+  if (c > 0.f) {
+    const float u = scale / c;
+    if (!std::isnormal(u) || !std::isfinite(u * 4.f) || !std::isnormal(0.625f / u) ||
+        !std::isnormal(c) || !std::isfinite(c * 2.f))
+      return FA_ERR_INVALID_ARG;
+  }
+  if (score->prefix_lengths != nullptr) {
+    if ((reinterpret_cast<uintptr_t>(score->prefix_lengths) & 3u) != 0) return FA_ERR_MISALIGNED;
+    if (!causal) return FA_ERR_INVALID_ARG;
+    if (window.left >= 0) return FA_ERR_UNSUPPORTED;
+  }
+  x->softcap = c;
+  x->prefix = score->prefix_lengths;
+  if (x->scored() && x->fused) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
 
@@ -602,6 +635,19 @@ fa_status_t fa_fwd_alibi(const void* q, const void* k, const void* v, void* o, f
   return forward(q, k, v, o, lse, B, H, N, d, scale, causal, window, x, stream);
 }
 
+fa_status_t fa_fwd_score(const void* q, const void* k, const void* v, void* o, float* lse, int B,
+                         int H, int N, int d, float scale, int causal, fa_window_t window,
+                         const fa_options_t* options, const fa_score_t* score, void* stream) {
+  bool empty;
+  fa_status_t s = check_problem(B, H, N, d, &empty);
+  if (s != FA_OK || empty) return s;
+  Extras x;
+  if ((s = resolve_options(options, &x)) != FA_OK) return s;
+  if ((s = check_mask(scale, window)) != FA_OK) return s;
+  if ((s = resolve_score(score, scale, causal, window, &x)) != FA_OK) return s;
+  return forward(q, k, v, o, lse, B, H, N, d, scale, causal, window, x, stream);
+}
+
 size_t fa_bwd_workspace_bytes(int B, int H, int N, int d) {
   bool empty;
   if (check_problem(B, H, N, d, &empty) != FA_OK || empty) return 0;
@@ -681,6 +727,24 @@ fa_status_t fa_bwd_ex(const void* q, const void* k, const void* v, const void* o
   if (s != FA_OK || empty) return s;
   Extras x;
   if ((s = resolve_options(options, &x)) != FA_OK) return s;
+  if ((s = check_ptrs({workspace})) != FA_OK) return s;
+  if (workspace_bytes_given < workspace_bytes(B, H, N, d, x)) return FA_ERR_WORKSPACE;
+  return backward(q, k, v, o, dout, lse, dq, dk, dv, B, H, N, d, scale, causal, window, x,
+                  workspace, stream);
+}
+
+fa_status_t fa_bwd_score(const void* q, const void* k, const void* v, const void* o,
+                         const void* dout, const float* lse, void* dq, void* dk, void* dv, int B,
+                         int H, int N, int d, float scale, int causal, fa_window_t window,
+                         const fa_options_t* options, const fa_score_t* score, void* workspace,
+                         size_t workspace_bytes_given, void* stream) {
+  bool empty;
+  fa_status_t s =
+      check_backward(q, k, v, o, dout, lse, dq, dk, dv, B, H, N, d, scale, window, &empty);
+  if (s != FA_OK || empty) return s;
+  Extras x;
+  if ((s = resolve_options(options, &x)) != FA_OK) return s;
+  if ((s = resolve_score(score, scale, causal, window, &x)) != FA_OK) return s;
   if ((s = check_ptrs({workspace})) != FA_OK) return s;
   if (workspace_bytes_given < workspace_bytes(B, H, N, d, x)) return FA_ERR_WORKSPACE;
   return backward(q, k, v, o, dout, lse, dq, dk, dv, B, H, N, d, scale, causal, window, x,
@@ -798,11 +862,15 @@ const char* fa_status_string(fa_status_t status) {
 fa_status_t fa_debug_status(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
   // every kernel unit has its own copy of the status word: read and clear them all
-  const int words[9] = {fa_host::take_status_fwd64(),  fa_host::take_status_fwd128(),
+  const int words[17] = {fa_host::take_status_fwd64(),  fa_host::take_status_fwd128(),
                         fa_host::take_status_bwd64(),  fa_host::take_status_bwd128(),
                         fa_host::take_status_fused64(), fa_host::take_status_fwdp64(),
                         fa_host::take_status_fwdp128(), fa_host::take_status_bwdp64(),
-                        fa_host::take_status_bwdp128()};
+                        fa_host::take_status_bwdp128(), fa_host::take_status_fwds64(),
+                        fa_host::take_status_fwds128(), fa_host::take_status_fwdsp64(),
+                        fa_host::take_status_fwdsp128(), fa_host::take_status_bwds64(),
+                        fa_host::take_status_bwds128(), fa_host::take_status_bwdsp64(),
+                        fa_host::take_status_bwdsp128()};
   bool timeout = false;
   for (int w : words) {
     if (w < 0) return FA_ERR_CUDA;

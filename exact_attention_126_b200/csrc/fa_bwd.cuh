@@ -34,6 +34,7 @@
 #include <cuda_bf16.h>
 
 #include "rng.cuh"
+#include "score.cuh"
 #include "sm100.cuh"
 #include "tiles.cuh"
 
@@ -208,6 +209,8 @@ struct BwdArgs {
   int total;            // LSE (H, total)), or null
   int sorted;           // variable-length batch: the schedule of varlen_item, with ...
   const int* sched;     // ... its tables, written by fa_bwd_preprocess_kernel
+  const int* prefix;    // kFeatScore: B prefix lengths, or null
+  CapArgs cap;          // kFeatScore: the cap of the scores
 };
 
 // Shared layout of both backward kernels: the stationary tiles X0, X1 of an item (in XB
@@ -348,7 +351,7 @@ __device__ __forceinline__ constexpr uint32_t packed_col(int kk) {
 // Returns false when the stationary tile lies past the sequence's real length (a
 // variable-length batch): such an item has no work, and every role skips it without
 // advancing its counters. `mk` is the item's mask, over the real length.
-template <bool kPacked = false>
+template <bool kPacked = false, bool kScore = false>
 __device__ __forceinline__ bool bwd_item(int k, const BwdArgs& a, bool rising, int& bh,
                                          int& tile, Mask& mk) {
   const int* const cu = kPacked ? a.cu : nullptr;
@@ -358,7 +361,7 @@ __device__ __forceinline__ bool bwd_item(int k, const BwdArgs& a, bool rising, i
     int u;
     if (!varlen_item(k, (int)gridDim.x, a.sched, a.n_tiles, a.H, bh, u)) return false;
     const int n = real_length(a.seq_len, cu, bh, a.H, a.N);
-    mk = Mask{n, a.left, a.right};
+    mk = Mask{n, a.left, a.right, kScore ? real_prefix(a.prefix, bh, a.H, n) : 0};
     // key tiles count from the end of the sequence, query tiles from its start
     tile = rising ? num_tiles(n) - 1 - u : u;
     return true;
@@ -369,7 +372,7 @@ __device__ __forceinline__ bool bwd_item(int k, const BwdArgs& a, bool rising, i
     tile = k % a.n_tiles;
   }
   const int n = real_length(a.seq_len, cu, bh, a.H, a.N);
-  mk = Mask{n, a.left, a.right};
+  mk = Mask{n, a.left, a.right, kScore ? real_prefix(a.prefix, bh, a.H, n) : 0};
   return tile < num_tiles(n);
 }
 
@@ -430,6 +433,7 @@ __global__ void __launch_bounds__(DkdvCfg<D>::kThreads, 1)
   constexpr bool kKpad = (kFeat & kFeatKpad) != 0;
   constexpr bool kDropout = (kFeat & kFeatDropout) != 0;
   constexpr bool kPacked = (kFeat & kFeatPacked) != 0;
+  constexpr bool kScore = (kFeat & kFeatScore) != 0;
   const int* const cu = kPacked ? a.cu : nullptr;  // a packed batch's cumulative lengths
   constexpr int kSBufs = (D == 64) ? 2 : 1;
   constexpr bool kDsInS = kSBufs == 2;               // dS^T over the second half of S^T
@@ -518,7 +522,7 @@ __global__ void __launch_bounds__(DkdvCfg<D>::kThreads, 1)
       for (int k = blockIdx.x; ok && k < a.n_items; k += gridDim.x) {
         int bh, j;
         Mask mk;
-        if (!bwd_item<kPacked>(k, a, true, bh, j, mk)) continue;
+        if (!bwd_item<kPacked, kScore>(k, a, true, bh, j, mk)) continue;
         int i_lo, i_hi;
         q_tiles_for_kv_tile(j, mk, i_lo, i_hi);
         const int xb = items % C::kXBufs, xu = items / C::kXBufs;
@@ -569,7 +573,7 @@ __global__ void __launch_bounds__(DkdvCfg<D>::kThreads, 1)
       for (int k = blockIdx.x; ok && k < a.n_items; k += gridDim.x) {
         int bh, j;
         Mask mk;
-        if (!bwd_item<kPacked>(k, a, true, bh, j, mk)) continue;
+        if (!bwd_item<kPacked, kScore>(k, a, true, bh, j, mk)) continue;
         int i_lo, i_hi;
         q_tiles_for_kv_tile(j, mk, i_lo, i_hi);
         const int xb = items % C::kXBufs, xu = items / C::kXBufs;
@@ -684,7 +688,7 @@ __global__ void __launch_bounds__(DkdvCfg<D>::kThreads, 1)
       for (int k = blockIdx.x; ok && k < a.n_items; k += gridDim.x) {
         int bh, j;
         Mask mk;
-        if (!bwd_item<kPacked>(k, a, true, bh, j, mk)) continue;
+        if (!bwd_item<kPacked, kScore>(k, a, true, bh, j, mk)) continue;
         int i_lo, i_hi;
         q_tiles_for_kv_tile(j, mk, i_lo, i_hi);
         for (int i = i_lo; i <= i_hi; ++i, ++t) {
@@ -793,7 +797,7 @@ __global__ void __launch_bounds__(DkdvCfg<D>::kThreads, 1)
       for (int k = blockIdx.x; k < a.n_items; k += gridDim.x) {
         int bh, j;
         Mask mk;
-        if (!bwd_item<kPacked>(k, a, true, bh, j, mk)) continue;
+        if (!bwd_item<kPacked, kScore>(k, a, true, bh, j, mk)) continue;
         const int xb = items % C::kXBufs;
         if (!mbar_wait(bar(bStaged), items & 1, abort_flag)) break;
         ++items;
@@ -821,13 +825,13 @@ __global__ void __launch_bounds__(DkdvCfg<D>::kThreads, 1)
     const int h = warp >> 2;              // query columns NC*h .. NC*h+NC-1 of each tile
     const int t_row = threadIdx.x & 127;  // key row in the tile == TMEM lane
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const float sl2 = a.scale_log2;
+    const float sl2 = kScore && a.cap.on ? a.cap.mul : a.scale_log2;
     int g = 0, items = 0;
     bool ok = true;
     for (int k = blockIdx.x; ok && k < a.n_items; k += gridDim.x) {
       int bh, j;
       Mask mk;
-      if (!bwd_item<kPacked>(k, a, true, bh, j, mk)) continue;
+      if (!bwd_item<kPacked, kScore>(k, a, true, bh, j, mk)) continue;
       int i_lo, i_hi;
       q_tiles_for_kv_tile(j, mk, i_lo, i_hi);
       const int n_it = i_hi - i_lo + 1;
@@ -865,45 +869,71 @@ __global__ void __launch_bounds__(DkdvCfg<D>::kThreads, 1)
         float p[NC];
         const uint32_t tSb = tmem + lane_base + tS + 128u * (t % kSBufs) + NC * h;
         load_cols32(tSb, p);
-#pragma unroll
-        for (int r = 0; r < NC; r += 4) {
-          const float4 l4 = *reinterpret_cast<const float4*>(lse_s + r);
-          float b4[4] = {0.f, 0.f, 0.f, 0.f};
-          if (kAlibi) {
-            // -m |query - key| in log2 units for the queries of these four columns
-            const float base = (float)((long long)i * kBlock + NC * h + r - c);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) b4[e] = -slope2 * fabsf(base + (float)e);
+        if constexpr (kScore) {
+          // visible queries of this key: bit r for query NC*h + r of the tile
+          uint32_t vis = ~0u;
+          if (!tile_all_visible(i, j, mk)) {
+            int r_lo, r_hi;
+            visible_queries(c, (long long)i * kBlock + NC * h, NC, mk, r_lo, r_hi);
+            vis = bit_range(r_lo, r_hi);
           }
-          p[r] = ex2(fmaf(p[r], sl2, kAlibi ? b4[0] - l4.x : -l4.x));
-          p[r + 1] = ex2(fmaf(p[r + 1], sl2, kAlibi ? b4[1] - l4.y : -l4.y));
-          p[r + 2] = ex2(fmaf(p[r + 2], sl2, kAlibi ? b4[2] - l4.z : -l4.z));
-          p[r + 3] = ex2(fmaf(p[r + 3], sl2, kAlibi ? b4[3] - l4.w : -l4.w));
-        }
-        if (!tile_all_visible(i, j, mk)) {
-          int r_lo, r_hi;
-          visible_queries(c, (long long)i * kBlock + NC * h, NC, mk, r_lo, r_hi);
-#pragma unroll
-          for (int r = 0; r < NC; ++r) p[r] = (r >= r_lo && r <= r_hi) ? p[r] : 0.f;
-        }
-        if (kKpad) {
-#pragma unroll
-          for (int r = 0; r < NC; ++r) p[r] = key_padded ? 0.f : p[r];
-        }
-        {
+          if (kKpad && key_padded) vis = 0u;
+          const float base = (float)((long long)i * kBlock + NC * h - c);
           uint32_t pk[NC / 2];
-          if (kDropout) {
-            // the weights that multiplied V: P o Z / (1 - p')
-            const float ks = a.drop.keep_scale;
-#pragma unroll
-            for (int r = 0; r < NC / 2; ++r)
-              pk[r] = pack_bf16x2(((keep >> (2 * r)) & 1u) ? p[2 * r] * ks : 0.f,
-                                  ((keep >> (2 * r + 1)) & 1u) ? p[2 * r + 1] * ks : 0.f);
-          } else {
-#pragma unroll
-            for (int r = 0; r < NC / 2; ++r) pk[r] = pack_bf16x2(p[2 * r], p[2 * r + 1]);
-          }
+          score_weights<kDropout>(
+              p, pk, a.cap, sl2, vis, keep, kDropout ? a.drop.keep_scale : 1.f, [&](int r) {
+                float4 l4 = *reinterpret_cast<const float4*>(lse_s + r);
+                l4 = make_float4(-l4.x, -l4.y, -l4.z, -l4.w);
+                if (kAlibi) {
+                  l4.x -= slope2 * fabsf(base + (float)r);
+                  l4.y -= slope2 * fabsf(base + (float)(r + 1));
+                  l4.z -= slope2 * fabsf(base + (float)(r + 2));
+                  l4.w -= slope2 * fabsf(base + (float)(r + 3));
+                }
+                return l4;
+              });
           tmem_st16(tSb, pk);
+        } else {
+#pragma unroll
+          for (int r = 0; r < NC; r += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(lse_s + r);
+            float b4[4] = {0.f, 0.f, 0.f, 0.f};
+            if (kAlibi) {
+              // -m |query - key| in log2 units for the queries of these four columns
+              const float base = (float)((long long)i * kBlock + NC * h + r - c);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) b4[e] = -slope2 * fabsf(base + (float)e);
+            }
+            p[r] = ex2(fmaf(p[r], sl2, kAlibi ? b4[0] - l4.x : -l4.x));
+            p[r + 1] = ex2(fmaf(p[r + 1], sl2, kAlibi ? b4[1] - l4.y : -l4.y));
+            p[r + 2] = ex2(fmaf(p[r + 2], sl2, kAlibi ? b4[2] - l4.z : -l4.z));
+            p[r + 3] = ex2(fmaf(p[r + 3], sl2, kAlibi ? b4[3] - l4.w : -l4.w));
+          }
+          if (!tile_all_visible(i, j, mk)) {
+            int r_lo, r_hi;
+            visible_queries(c, (long long)i * kBlock + NC * h, NC, mk, r_lo, r_hi);
+#pragma unroll
+            for (int r = 0; r < NC; ++r) p[r] = (r >= r_lo && r <= r_hi) ? p[r] : 0.f;
+          }
+          if (kKpad) {
+#pragma unroll
+            for (int r = 0; r < NC; ++r) p[r] = key_padded ? 0.f : p[r];
+          }
+          {
+            uint32_t pk[NC / 2];
+            if (kDropout) {
+              // the weights that multiplied V: P o Z / (1 - p')
+              const float ks = a.drop.keep_scale;
+#pragma unroll
+              for (int r = 0; r < NC / 2; ++r)
+                pk[r] = pack_bf16x2(((keep >> (2 * r)) & 1u) ? p[2 * r] * ks : 0.f,
+                                    ((keep >> (2 * r + 1)) & 1u) ? p[2 * r + 1] * ks : 0.f);
+            } else {
+#pragma unroll
+              for (int r = 0; r < NC / 2; ++r) pk[r] = pack_bf16x2(p[2 * r], p[2 * r + 1]);
+            }
+            tmem_st16(tSb, pk);
+          }
         }
         tmem_wait_st();
         tc_fence_before();
@@ -1013,6 +1043,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1)
   constexpr bool kKpad = (kFeat & kFeatKpad) != 0;
   constexpr bool kDropout = (kFeat & kFeatDropout) != 0;
   constexpr bool kPacked = (kFeat & kFeatPacked) != 0;
+  constexpr bool kScore = (kFeat & kFeatScore) != 0;
   const int* const cu = kPacked ? a.cu : nullptr;  // a packed batch's cumulative lengths
   constexpr uint32_t tS0 = 0, tDP = 256, tDQ = 384;
   // per S buffer: S full, dS full, dQ done (dQ read that buffer's dS); dP full, dP free;
@@ -1069,7 +1100,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1)
       for (int k = blockIdx.x; ok && k < a.n_items; k += gridDim.x) {
         int bh, i;
         Mask mk;
-        if (!bwd_item<kPacked>(k, a, false, bh, i, mk)) continue;
+        if (!bwd_item<kPacked, kScore>(k, a, false, bh, i, mk)) continue;
         int j_lo, j_hi;
         kv_tiles_for_q_tile(i, mk, j_lo, j_hi);
         const int xb = items % C::kXBufs, xu = items / C::kXBufs;
@@ -1124,7 +1155,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1)
       for (int k = blockIdx.x; ok && k < a.n_items; k += gridDim.x) {
         int bh, i;
         Mask mk;
-        if (!bwd_item<kPacked>(k, a, false, bh, i, mk)) continue;
+        if (!bwd_item<kPacked, kScore>(k, a, false, bh, i, mk)) continue;
         int j_lo, j_hi;
         kv_tiles_for_q_tile(i, mk, j_lo, j_hi);
         const int xb = items % C::kXBufs, xu = items / C::kXBufs;
@@ -1190,7 +1221,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1)
       for (int k = blockIdx.x; ok && k < a.n_items; k += gridDim.x) {
         int bh, i;
         Mask mk;
-        if (!bwd_item<kPacked>(k, a, false, bh, i, mk)) continue;
+        if (!bwd_item<kPacked, kScore>(k, a, false, bh, i, mk)) continue;
         int j_lo, j_hi;
         kv_tiles_for_q_tile(i, mk, j_lo, j_hi);
         for (int jj = j_lo; jj <= j_hi; ++jj, ++t) {
@@ -1230,7 +1261,7 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1)
       for (int k = blockIdx.x; k < a.n_items; k += gridDim.x) {
         int bh, i;
         Mask mk;
-        if (!bwd_item<kPacked>(k, a, false, bh, i, mk)) continue;
+        if (!bwd_item<kPacked, kScore>(k, a, false, bh, i, mk)) continue;
         const int xb = items % C::kXBufs;
         if (!mbar_wait(bar(bStaged), items & 1, abort_flag)) break;
         ++items;
@@ -1254,13 +1285,13 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1)
     const int h = warp >> 2;          // key columns NC*h .. NC*h+NC-1 of each key tile
     const int t_row = threadIdx.x & 127;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const float sl2 = a.scale_log2;
+    const float sl2 = kScore && a.cap.on ? a.cap.mul : a.scale_log2;
     int g = 0, items = 0;
     bool ok = true;
     for (int k = blockIdx.x; ok && k < a.n_items; k += gridDim.x) {
       int bh, i;
       Mask mk;
-      if (!bwd_item<kPacked>(k, a, false, bh, i, mk)) continue;
+      if (!bwd_item<kPacked, kScore>(k, a, false, bh, i, mk)) continue;
       int j_lo, j_hi;
       kv_tiles_for_q_tile(i, mk, j_lo, j_hi);
       const int n_it = j_hi - j_lo + 1;
@@ -1287,41 +1318,68 @@ __global__ void __launch_bounds__(DqCfg<D>::kThreads, 1)
         tc_fence_after();
         float p[NC];
         load_cols32(tmem + lane_base + tS0 + 128u * b + NC * h, p);
-        {
-          // with ALiBi, -m |key - query| in log2 units joins the exponent
+        if constexpr (kScore) {
+          // visible keys of this query: bit c for key NC*h + c of the tile
+          uint32_t vis = ~0u;
+          if (!tile_all_visible(i, jj, mk)) {
+            int c_lo, c_hi;
+            visible_keys(r, (long long)jj * kBlock + NC * h, NC, mk, c_lo, c_hi);
+            vis = bit_range(c_lo, c_hi);
+          }
+          if (kKpad) {
+            const int col = jj * kBlock + NC * h + lane;
+            vis &= ~__ballot_sync(
+                0xffffffffu, col < a.N && a.kpad[(size_t)(bh / a.H) * a.N + col] != 0);
+          }
           const float base = (float)((long long)jj * kBlock + NC * h - r);
-          if constexpr (kAlibi) {
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              const float arg = -slope2 * fabsf(base + (float)c) - lse2;
-              p[c] = ex2(fmaf(p[c], sl2, arg));
+          uint32_t pk[NC / 2];  // (P itself is not used here)
+          score_weights<false>(p, pk, a.cap, sl2, vis, ~0u, 1.f, [&](int c) {
+            float4 v = make_float4(-lse2, -lse2, -lse2, -lse2);
+            if (kAlibi) {
+              v.x -= slope2 * fabsf(base + (float)c);
+              v.y -= slope2 * fabsf(base + (float)(c + 1));
+              v.z -= slope2 * fabsf(base + (float)(c + 2));
+              v.w -= slope2 * fabsf(base + (float)(c + 3));
             }
-          } else {
-            // exponent arguments two at a time (packed fp32 FMA), rounded as fmaf rounds
-            const float2 s2 = make_float2(sl2, sl2), a2 = make_float2(-lse2, -lse2);
+            return v;
+          });
+        } else {
+          {
+            // with ALiBi, -m |key - query| in log2 units joins the exponent
+            const float base = (float)((long long)jj * kBlock + NC * h - r);
+            if constexpr (kAlibi) {
 #pragma unroll
-            for (int c = 0; c < NC; c += 2) {
-              const float2 x = __ffma2_rn(make_float2(p[c], p[c + 1]), s2, a2);
-              p[c] = ex2(x.x);
-              p[c + 1] = ex2(x.y);
+              for (int c = 0; c < NC; ++c) {
+                const float arg = -slope2 * fabsf(base + (float)c) - lse2;
+                p[c] = ex2(fmaf(p[c], sl2, arg));
+              }
+            } else {
+              // exponent arguments two at a time (packed fp32 FMA), rounded as fmaf rounds
+              const float2 s2 = make_float2(sl2, sl2), a2 = make_float2(-lse2, -lse2);
+#pragma unroll
+              for (int c = 0; c < NC; c += 2) {
+                const float2 x = __ffma2_rn(make_float2(p[c], p[c + 1]), s2, a2);
+                p[c] = ex2(x.x);
+                p[c + 1] = ex2(x.y);
+              }
             }
           }
-        }
-        if (!tile_all_visible(i, jj, mk)) {
-          int c_lo, c_hi;
-          visible_keys(r, (long long)jj * kBlock + NC * h, NC, mk, c_lo, c_hi);
+          if (!tile_all_visible(i, jj, mk)) {
+            int c_lo, c_hi;
+            visible_keys(r, (long long)jj * kBlock + NC * h, NC, mk, c_lo, c_hi);
 #pragma unroll
-          for (int c = 0; c < NC; ++c) p[c] = (c >= c_lo && c <= c_hi) ? p[c] : 0.f;
-        }
-        if (kKpad) {
-          // lane l reads the flag of key NC*h + l of the tile; the ballot gives all 32
-          static_assert(NC == 32, "one ballot covers a warpgroup's columns");
-          const int col = jj * kBlock + NC * h + lane;
-          const uint32_t pm = __ballot_sync(
-              0xffffffffu, col < a.N && a.kpad[(size_t)(bh / a.H) * a.N + col] != 0);
-          if (pm != 0u) {
+            for (int c = 0; c < NC; ++c) p[c] = (c >= c_lo && c <= c_hi) ? p[c] : 0.f;
+          }
+          if (kKpad) {
+            // lane l reads the flag of key NC*h + l of the tile; the ballot gives all 32
+            static_assert(NC == 32, "one ballot covers a warpgroup's columns");
+            const int col = jj * kBlock + NC * h + lane;
+            const uint32_t pm = __ballot_sync(
+                0xffffffffu, col < a.N && a.kpad[(size_t)(bh / a.H) * a.N + col] != 0);
+            if (pm != 0u) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c) p[c] = ((pm >> c) & 1u) ? 0.f : p[c];
+              for (int c = 0; c < NC; ++c) p[c] = ((pm >> c) & 1u) ? 0.f : p[c];
+            }
           }
         }
         if (!mbar_wait_warp(bar(bDPFull), t & 1, abort_flag)) {

@@ -34,6 +34,7 @@
 #include <cuda_bf16.h>
 
 #include "rng.cuh"
+#include "score.cuh"
 #include "sm100.cuh"
 #include "tiles.cuh"
 
@@ -68,6 +69,8 @@ struct FwdArgs {
   int sorted;                // variable-length batch: the schedule of varlen_item, whose
                              // tables each CTA builds in shared memory after kMisc
   float o_scale;             // kFeatFp8: the V descale, applied to O in the epilogue
+  const int* prefix;         // kFeatScore: B prefix lengths, or null
+  CapArgs cap;               // kFeatScore: the cap of the scores
 };
 
 // kFp8: 8-bit (e4m3) Q, K, V tiles (head_dim 128 only: one 128-byte row per token).
@@ -137,6 +140,7 @@ struct FwdCfg {
 struct FwdItem {
   int bh;
   int n;        // the sequence's real length (N unless the batch is variable-length)
+  int prefix;   // keys every query sees (kFeatScore)
   int m[2];
   bool has_a;   // query tile A lies within the real length (else the item has no work)
   bool has_b;
@@ -150,6 +154,7 @@ __device__ __forceinline__ FwdItem no_fwd_item() {
   FwdItem it;
   it.bh = 0;
   it.n = 0;
+  it.prefix = 0;
   it.m[0] = it.m[1] = 0;
   it.has_a = it.has_b = false;
   it.lo[0] = it.lo[1] = 1;
@@ -160,8 +165,8 @@ __device__ __forceinline__ FwdItem no_fwd_item() {
 }
 
 // `sched`: the varlen_item tables (shared memory) when a.sorted; kPacked: a packed batch
-// (a.cu), else a.cu is not looked at.
-template <bool kPacked>
+// (a.cu), else a.cu is not looked at; kScore: a.prefix likewise.
+template <bool kPacked, bool kScore>
 __device__ __forceinline__ FwdItem fwd_item(int k, const FwdArgs& a, const int* sched) {
   const int* const cu = kPacked ? a.cu : nullptr;
   FwdItem it;
@@ -179,7 +184,8 @@ __device__ __forceinline__ FwdItem fwd_item(int k, const FwdArgs& a, const int* 
     pair = k % a.n_pairs;
   }
   it.n = real_length(a.seq_len, cu, it.bh, a.H, a.N);
-  const Mask mk{it.n, a.left, a.right};
+  it.prefix = kScore ? real_prefix(a.prefix, it.bh, a.H, it.n) : 0;
+  const Mask mk{it.n, a.left, a.right, it.prefix};
   const int n_qtiles = num_tiles(it.n);
   it.m[0] = a.per_item * pair;
   it.m[1] = it.m[0] + 1;
@@ -224,7 +230,9 @@ __device__ __forceinline__ FwdRange fwd_range(const FwdItem& it, int s) {
 // clear before the P V product (the row sum l keeps them: dropout follows the softmax)
 // and scales O by 1 / (1 - p'); kFeatFp8 takes e4m3 Q, K, V (S = Q K^T and P V as
 // kind::f8f6f4 products, P rounded to e4m3, four per tensor-memory column; the Q and K
-// descales are folded into scale_log2, the V descale into O).
+// descales are folded into scale_log2, the V descale into O); kFeatScore caps the scores by
+// c tanh(s / c) as they are loaded (score.cuh; a.cap.on) and shows the first a.prefix[b] keys
+// to every query, both optional at run time.
 // 352 threads (11 warps, three of them on one SM sub-partition with its 16K registers): at
 // most 168 registers per thread.
 template <int D, int kFeat = 0>
@@ -238,6 +246,7 @@ __global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 
   constexpr bool kResidual = (kFeat & kFeatResidual) != 0;
   constexpr bool kDropout = (kFeat & kFeatDropout) != 0;
   constexpr bool kPacked = (kFeat & kFeatPacked) != 0;
+  constexpr bool kScore = (kFeat & kFeatScore) != 0;
   const int* const cu = kPacked ? a.cu : nullptr;  // a packed batch's cumulative lengths
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -301,7 +310,7 @@ __global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 
       int kc = 0, vc = 0;  // K and V loads issued (ring positions)
       bool ok = true;
       for (int k = blockIdx.x; ok && k < a.n_items; k += gridDim.x) {
-        const FwdItem it = fwd_item<kPacked>(k, a, sched);
+        const FwdItem it = fwd_item<kPacked, kScore>(k, a, sched);
         if (!it.has_a) continue;  // past the real length: nothing to load
         const int base = seq_base(cu, it.bh, a.H);
         for (int s = 0; s < 2; ++s) {
@@ -547,7 +556,7 @@ __global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 
       };
 
       for (int k = blockIdx.x; ok && k < a.n_items; k += gridDim.x) {
-        const FwdItem it = fwd_item<kPacked>(k, a, sched);
+        const FwdItem it = fwd_item<kPacked, kScore>(k, a, sched);
         if (!it.has_a) continue;  // past the real length: no products
         const FwdRange rg = fwd_range(it, s);
         const int n = it.last - it.first + 1;
@@ -585,7 +594,8 @@ __global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 
     const uint32_t tS = tmem + lane_base + C::tS + 128u * s;
     const uint32_t tP = C::kSepP ? tmem + lane_base + C::tP + 64u * s : tS;
     const uint32_t tO = tmem + lane_base + C::tO + D * s;
-    const float sl2 = a.scale_log2;
+    // what turns a score (kFeatScore with a cap: its tanh) into log2 units
+    const float sl2 = kScore && a.cap.on ? a.cap.mul : a.scale_log2;
     int ns = 0;  // S tiles of this stream consumed (all items)
     int nsh[2] = {0, 0};   // kHalves: S halves consumed, per half
     int npub[2] = {0, 0};  // kHalves: P halves published, per half
@@ -593,10 +603,10 @@ __global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 
 
 
     for (int k = blockIdx.x; ok && k < a.n_items; k += gridDim.x) {
-      const FwdItem it = fwd_item<kPacked>(k, a, sched);
+      const FwdItem it = fwd_item<kPacked, kScore>(k, a, sched);
       const FwdRange rg = fwd_range(it, s);
       if (!rg.has) continue;
-      const Mask mk{it.n, a.left, a.right};
+      const Mask mk{it.n, a.left, a.right, it.prefix};
       const int row = rg.m * kBlock + r;
       // with ALiBi the scores are scaled and biased as they are loaded (in log2 units), so
       // the later steps take them as they are
@@ -634,6 +644,7 @@ __global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 
 #pragma unroll
               for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(u[c]);
             }
+            if (kScore && a.cap.on) cap_tanh(x, a.cap);
             if (kAlibi) {
               // key minus query index at column 0 of the half
               const long long kq = (long long)j * kBlock + 64 * h - row;
@@ -788,6 +799,7 @@ __global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 
           tc_fence_before();
           mbar_arrive_warp(bar(C::bSFree + s));
         }
+        if (kScore && a.cap.on) cap_tanh(x, a.cap);
         if (kAlibi) {
           // key minus query index at column 0 of the tile
           const long long kq = (long long)j * kBlock - row;

@@ -29,16 +29,21 @@ struct Extras {
   int total = 0;                   // ... the tokens of its (total, H, d) tensors
   bool fp8 = false;                // forward on e4m3 Q, K, V (the kFeatFp8 kernel)
   float o_scale = 1.f;             // with fp8: the V descale, applied to O
+  const int* prefix = nullptr;     // B prefix lengths: the kFeatScore kernels, as
+  float softcap = 0.f;             // ... a cap of the scores (0 = none)
   fa::DropoutArgs drop = {0, 0, 0, 0, 1.f};
 
   // A batch of sequences of their own lengths (padded or packed).
   bool varlen() const { return seq_len != nullptr || cu != nullptr; }
 
+  bool scored() const { return prefix != nullptr || softcap > 0.f; }
+
   // The kernel variant these options select (the backward passes ignore kFeatResidual).
   int features() const {
     return (alibi ? fa::kFeatAlibi : 0) | (kpad ? fa::kFeatKpad : 0) |
            (o_low ? fa::kFeatResidual : 0) | (dropout ? fa::kFeatDropout : 0) |
-           (fp8 ? fa::kFeatFp8 : 0) | (cu ? fa::kFeatPacked : 0);
+           (fp8 ? fa::kFeatFp8 : 0) | (cu ? fa::kFeatPacked : 0) |
+           (scored() ? fa::kFeatScore : 0);
   }
 };
 
@@ -105,5 +110,13 @@ int take_status_bwdp128();
 int take_status_bwd64();
 int take_status_bwd128();
 int take_status_fused64();
+int take_status_fwds64();
+int take_status_fwds128();
+int take_status_fwdsp64();
+int take_status_fwdsp128();
+int take_status_bwds64();
+int take_status_bwds128();
+int take_status_bwdsp64();
+int take_status_bwdsp128();
 
 }  // namespace fa_host

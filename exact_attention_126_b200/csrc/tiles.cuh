@@ -1,7 +1,8 @@
 // tiles.cuh - which (query tile, key tile) pairs carry work, and which scores are masked.
 //
 // A tile is 128 consecutive rows of one (batch, head). Key j is visible from query i iff
-// i - left <= j <= i + right (-1 = unbounded), both < N; causal masking forces right = 0
+// i - left <= j <= i + right (-1 = unbounded), both < N, or j lies in the sequence's prefix
+// (causal problems: a prefix is seen in both directions); causal masking forces right = 0
 // (page "告别OOM和训练慢…(含A100环境配置)" §4.2, `causal`, `window_size=(-1,-1)`; page
 // "Flash Attention 3.7 核心原理与实战" §3.2, "mask future positions"). Tiles whose every
 // score is masked are never visited; tiles whose every score is visible skip the
@@ -20,12 +21,14 @@ constexpr int kFeatResidual = 4;  // forward also writes O - bf16(O)
 constexpr int kFeatDropout = 8;   // attention weights dropped with Philox keep flags
 constexpr int kFeatFp8 = 16;      // forward on e4m3 Q, K, V (P in e4m3 for the P V product)
 constexpr int kFeatPacked = 32;   // a packed batch: (total, H, D) tensors, cumulative lengths
+constexpr int kFeatScore = 64;    // scores capped by a tanh and / or a prefix seen by all queries
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Mask {
   int N;      // sequence length
   int left;   // -1 = unbounded
   int right;  // -1 = unbounded, 0 when causal
+  int prefix = 0;  // keys below it are visible from every query, whatever `right` (left = -1)
 };
 
 __host__ __device__ inline int resolve_right(int causal, int right) {
@@ -50,6 +53,13 @@ __device__ __forceinline__ int real_length(const int* seq_len, const int* cu, in
     return N;
   }
   return L < 0 ? 0 : (L > N ? N : L);
+}
+
+// The prefix of bh's sequence (real length L): prefix[bh / H] clamped to [0, L], 0 without.
+__device__ __forceinline__ int real_prefix(const int* prefix, int bh, int H, int L) {
+  if (prefix == nullptr) return 0;
+  const int p = __ldg(prefix + bh / H);
+  return p < 0 ? 0 : (p > L ? L : p);
 }
 
 // Where the rows of (batch, head) bh lie. Without cumulative lengths the tensors are
@@ -93,7 +103,10 @@ __host__ __device__ inline void kv_tiles_for_q_tile(int m, const Mask& k, int& l
   const long long r1 = (r0 + kBlock < k.N ? r0 + kBlock : k.N) - 1;
   long long c0 = 0, c1 = k.N - 1;
   if (k.left >= 0 && r0 - k.left > c0) c0 = r0 - k.left;
-  if (k.right >= 0 && r1 + k.right < c1) c1 = r1 + k.right;
+  if (k.right >= 0 && r1 + k.right < c1) {
+    c1 = r1 + k.right;
+    if (k.prefix > 0 && k.prefix - 1 > c1) c1 = k.prefix - 1 < k.N - 1 ? k.prefix - 1 : k.N - 1;
+  }
   lo = (int)(c0 / kBlock);
   hi = (int)(c1 / kBlock);
 }
@@ -103,7 +116,7 @@ __host__ __device__ inline void q_tiles_for_kv_tile(int j, const Mask& k, int& l
   const long long c0 = (long long)j * kBlock;
   const long long c1 = (c0 + kBlock < k.N ? c0 + kBlock : k.N) - 1;
   long long r0 = 0, r1 = k.N - 1;
-  if (k.right >= 0 && c0 - k.right > r0) r0 = c0 - k.right;
+  if (k.right >= 0 && c0 - k.right > r0 && !(k.prefix > 0 && c0 < k.prefix)) r0 = c0 - k.right;
   if (k.left >= 0 && c1 + k.left < r1) r1 = c1 + k.left;
   lo = (int)(r0 / kBlock);
   hi = (int)(r1 / kBlock);
@@ -114,14 +127,14 @@ __host__ __device__ inline bool tile_all_visible(int qt, int kt, const Mask& k) 
   const long long r0 = (long long)qt * kBlock, r1 = r0 + kBlock - 1;
   const long long c0 = (long long)kt * kBlock, c1 = c0 + kBlock - 1;
   if (r1 >= k.N || c1 >= k.N) return false;
-  if (k.right >= 0 && c1 - r0 > k.right) return false;
+  if (k.right >= 0 && c1 - r0 > k.right && !(k.prefix > 0 && c1 < k.prefix)) return false;
   if (k.left >= 0 && r1 - c0 > k.left) return false;
   return true;
 }
 
 __host__ __device__ inline bool is_visible(int r, int c, const Mask& k) {
   return r < k.N && c < k.N && (k.left < 0 || r - c <= k.left) &&
-         (k.right < 0 || c - r <= k.right);
+         (k.right < 0 || c - r <= k.right || c < k.prefix);
 }
 
 // Keys col_base + [c_lo, c_hi] of the `width` keys from col_base that query `row` sees
@@ -131,7 +144,11 @@ __host__ __device__ inline void visible_keys(int row, long long col_base, int wi
                                              const Mask& k, int& c_lo, int& c_hi) {
   long long lo = 0, hi = width - 1;
   if (k.left >= 0 && row - k.left - col_base > lo) lo = row - k.left - col_base;
-  if (k.right >= 0 && row + (long long)k.right - col_base < hi) hi = row + (long long)k.right - col_base;
+  if (k.right >= 0 && row + (long long)k.right - col_base < hi) {
+    const long long own = row + (long long)k.right - col_base;
+    const long long pre = k.prefix > 0 ? k.prefix - 1 - col_base : own;
+    hi = own > pre ? own : (pre < hi ? pre : hi);
+  }
   if (k.N - 1 - col_base < hi) hi = k.N - 1 - col_base;
   if (row >= k.N) hi = -1;
   c_lo = (int)(lo > width ? width : lo);
@@ -143,7 +160,8 @@ __host__ __device__ inline void visible_keys(int row, long long col_base, int wi
 __host__ __device__ inline void visible_queries(int col, long long row_base, int width,
                                                 const Mask& k, int& r_lo, int& r_hi) {
   long long lo = 0, hi = width - 1;
-  if (k.right >= 0 && col - k.right - row_base > lo) lo = col - k.right - row_base;
+  if (k.right >= 0 && col - k.right - row_base > lo && !(k.prefix > 0 && col < k.prefix))
+    lo = col - k.right - row_base;
   if (k.left >= 0 && col + (long long)k.left - row_base < hi) hi = col + (long long)k.left - row_base;
   if (k.N - 1 - row_base < hi) hi = k.N - 1 - row_base;
   if (col >= k.N) hi = -1;

@@ -27,7 +27,8 @@ STATUS_NAMES = {
 EXPORTED = ("fa_fwd", "fa_fwd_ex", "fa_fwd_fp8", "fa_bwd_workspace_bytes",
             "fa_bwd_workspace_bytes_ex", "fa_bwd", "fa_bwd_ex",
             "fa_fwd_alibi", "fa_bwd_alibi", "fa_bwd_preprocess", "fa_bwd_dkdv", "fa_bwd_dq",
-            "fa_bwd_fused", "fa_bwd_dq_convert", "fa_bwd_noalloc", "fa_qk_norm_rope_fwd",
+            "fa_bwd_fused", "fa_bwd_dq_convert", "fa_bwd_noalloc", "fa_fwd_score",
+            "fa_bwd_score", "fa_qk_norm_rope_fwd",
             "fa_qk_norm_rope_workspace_bytes", "fa_qk_norm_rope_bwd", "fa_status_string",
             "fa_debug_status", "fa_debug_set_fault", "fa_version")
 
@@ -53,6 +54,11 @@ class fa_options_t(ctypes.Structure):
                 ("flags", ctypes.c_uint), ("dropout_seed", ctypes.c_ulonglong),
                 ("dropout_offset", ctypes.c_ulonglong), ("seq_lengths", ctypes.c_void_p),
                 ("cu_seqlens", ctypes.c_void_p), ("total_tokens", ctypes.c_int)]
+
+
+class fa_score_t(ctypes.Structure):
+    """Changes to the scores of fa_fwd_score and fa_bwd_score (include/fa.h)."""
+    _fields_ = [("prefix_lengths", ctypes.c_void_p), ("softcap", ctypes.c_float)]
 
 
 class fa_heads_t(ctypes.Structure):
@@ -119,6 +125,10 @@ def _lib() -> ctypes.CDLL:
         lib.fa_bwd_dq_convert.argtypes = [vp, vp, I, I, I, I, F, vp]
         lib.fa_bwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, I, I, I, I, F, I, W,
                                        vp]
+        SP = ctypes.POINTER(fa_score_t)
+        lib.fa_fwd_score.argtypes = [vp, vp, vp, vp, vp, I, I, I, I, F, I, W, OP, SP, vp]
+        lib.fa_bwd_score.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, I, I, I, I, F, I, W, OP,
+                                     SP, vp, ctypes.c_size_t, vp]
         HP, NP = ctypes.POINTER(fa_heads_t), ctypes.POINTER(fa_norm_rope_t)
         lib.fa_qk_norm_rope_fwd.argtypes = [HP, HP, HP, HP, HP, HP, I, I, I, NP, vp]
         lib.fa_qk_norm_rope_bwd.argtypes = [HP, HP, HP, HP, HP, HP, HP, HP, vp, vp, I, I, I, NP,
@@ -132,8 +142,8 @@ def _lib() -> ctypes.CDLL:
         lib.fa_version.argtypes = []
         for name in ("fa_fwd", "fa_fwd_ex", "fa_fwd_fp8", "fa_bwd", "fa_bwd_ex", "fa_fwd_alibi",
                      "fa_bwd_alibi", "fa_bwd_preprocess", "fa_bwd_fused", "fa_bwd_dq_convert",
-                     "fa_bwd_dkdv", "fa_bwd_dq", "fa_bwd_noalloc", "fa_qk_norm_rope_fwd",
-                     "fa_qk_norm_rope_bwd", "fa_debug_status", "fa_debug_set_fault",
+                     "fa_bwd_dkdv", "fa_bwd_dq", "fa_bwd_noalloc", "fa_fwd_score", "fa_bwd_score",
+                     "fa_qk_norm_rope_fwd", "fa_qk_norm_rope_bwd", "fa_debug_status", "fa_debug_set_fault",
                      "fa_version"):
             getattr(lib, name).restype = I
         _LIB = lib
@@ -286,6 +296,29 @@ def fa_bwd_ex(q, k, v, o, do, lse, dq, dk, dv, workspace, opt=None, scale=None, 
                             _ptr(workspace), nbytes, _stream(stream)), "fa_bwd_ex")
 
 
+def fa_fwd_score(q, k, v, o, lse, opt=None, score=None, scale=None, causal=False,
+                 window=(-1, -1), stream=None, dims=None) -> None:
+    """fa_fwd_ex with an fa_score_t (a cap of the scores, prefix lengths)."""
+    B, H, N, d = _shape(q, dims)
+    c, w = _window(causal, window)
+    s = default_scale(d) if scale is None else float(scale)
+    _check(_lib().fa_fwd_score(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, N, d, s, c, w,
+                               _opt_ref(opt), _opt_ref(score), _stream(stream)), "fa_fwd_score")
+
+
+def fa_bwd_score(q, k, v, o, do, lse, dq, dk, dv, workspace, opt=None, score=None, scale=None,
+                 causal=False, window=(-1, -1), stream=None, dims=None) -> None:
+    """fa_bwd_ex with the fa_score_t the forward had."""
+    B, H, N, d = _shape(q, dims)
+    c, w = _window(causal, window)
+    s = default_scale(d) if scale is None else float(scale)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib().fa_bwd_score(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq),
+                               _ptr(dk), _ptr(dv), B, H, N, d, s, c, w, _opt_ref(opt),
+                               _opt_ref(score), _ptr(workspace), nbytes, _stream(stream)),
+           "fa_bwd_score")
+
+
 def fa_bwd_preprocess(o, do, lse, workspace, opt=None, stream=None, dims=None) -> None:
     B, H, N, d = _shape(o, dims)
     _check(_lib().fa_bwd_preprocess(_ptr(o), _ptr(do), _ptr(lse), _ptr(workspace), B, H, N, d,
@@ -425,9 +458,24 @@ def _packed_dims(q, cu_seqlens, max_seqlen, seq_lengths):
     return cu_seqlens.numel() - 1, int(q.shape[1]), int(max_seqlen), int(q.shape[2])
 
 
+def _score(softcap, prefix_lengths, q, B):
+    """The fa_score_t of a cap and prefix lengths, or None without either."""
+    if prefix_lengths is not None:
+        if not prefix_lengths.is_cuda or prefix_lengths.dtype != torch.int32:
+            raise ValueError("prefix_lengths must be an int32 CUDA tensor")
+        if tuple(prefix_lengths.shape) != (B,) or not prefix_lengths.is_contiguous():
+            raise ValueError("prefix_lengths must hold one length per sequence, contiguous")
+        if prefix_lengths.device != q.device:
+            raise ValueError("prefix_lengths must be on the queries' device")
+    elif softcap is None or softcap == 0.0:
+        return None
+    return fa_score_t(_ptr(prefix_lengths), 0.0 if softcap is None else float(softcap))
+
+
 def attention_forward(q, k, v, scale=None, causal=False, window=(-1, -1), stream=None,
                       alibi_slopes=None, key_padding=None, keep_residual=False, dropout=None,
-                      seq_lengths=None, cu_seqlens=None, max_seqlen=None):
+                      seq_lengths=None, cu_seqlens=None, max_seqlen=None, softcap=0.0,
+                      prefix_lengths=None):
     """Returns (O, LSE) for bf16 CUDA tensors q, k, v of shape (B, H, N, d), or
     (O, LSE, O_low) with keep_residual: O_low = O_fp32 - bf16(O) in bf16, which
     attention_backward uses to form rowsum(dO o O) from O to about 16 bits.
@@ -439,7 +487,9 @@ def attention_forward(q, k, v, scale=None, causal=False, window=(-1, -1), stream
     entry b holds seq_lengths[b] real tokens; rows past it are zero (LSE -inf) and tiles
     wholly past it are not computed. cu_seqlens ((B + 1,) int32) with max_seqlen: a packed
     batch, q, k, v of shape (total, H, d) holding sequence b at tokens cu_seqlens[b] ..
-    cu_seqlens[b+1]-1; O is (total, H, d) and LSE (H, total)."""
+    cu_seqlens[b+1]-1; O is (total, H, d) and LSE (H, total). softcap (c > 0): the scaled scores
+    s become c tanh(s / c). prefix_lengths ((B,) int32), for causal problems: query i of
+    sequence b also sees every key j < prefix_lengths[b]."""
     _check_inputs(q, k, v)
     if cu_seqlens is not None:
         B, H, N, d = _packed_dims(q, cu_seqlens, max_seqlen, seq_lengths)
@@ -455,23 +505,29 @@ def attention_forward(q, k, v, scale=None, causal=False, window=(-1, -1), stream
         _check_padding(key_padding, B, N)
     if seq_lengths is not None:
         _check_lengths(seq_lengths, q)
+    score = _score(softcap, prefix_lengths, q, B)
     if (alibi_slopes is None and key_padding is None and o_low is None and dropout is None
-            and seq_lengths is None and cu_seqlens is None):
+            and seq_lengths is None and cu_seqlens is None and score is None):
         fa_fwd(q, k, v, o, lse, scale, causal, window, stream)
     else:
         opt = options(alibi_slopes, key_padding, o_low, *(dropout or ()),
                       seq_lengths=seq_lengths, cu_seqlens=cu_seqlens,
                       total_tokens=q.shape[0] if cu_seqlens is not None else 0)
-        fa_fwd_ex(q, k, v, o, lse, opt, scale, causal, window, stream, dims=(B, H, N, d))
+        if score is None:
+            fa_fwd_ex(q, k, v, o, lse, opt, scale, causal, window, stream, dims=(B, H, N, d))
+        else:
+            fa_fwd_score(q, k, v, o, lse, opt, score, scale, causal, window, stream,
+                         dims=(B, H, N, d))
     return (o, lse, o_low) if keep_residual else (o, lse)
 
 
 def attention_backward(q, k, v, o, lse, do, scale=None, causal=False, window=(-1, -1),
                        stream=None, alibi_slopes=None, key_padding=None, o_low=None,
                        dropout=None, fused=False, seq_lengths=None, cu_seqlens=None,
-                       max_seqlen=None):
+                       max_seqlen=None, softcap=0.0, prefix_lengths=None):
     """Returns (dQ, dK, dV): the gradient of <O, dO>; lse (and o_low, if kept) come from
-    attention_forward with the same alibi_slopes, key_padding, dropout and seq_lengths.
+    attention_forward with the same alibi_slopes, key_padding, dropout, seq_lengths, softcap and
+    prefix_lengths.
     fused: at head_dim 64, the backward in one pass over key tiles with dQ added up in fp32
     in no fixed order (see FA_BWD_FUSED); otherwise the deterministic dK/dV and dQ passes."""
     _check_inputs(q, k, v, o, do)
@@ -495,15 +551,20 @@ def attention_backward(q, k, v, o, lse, do, scale=None, causal=False, window=(-1
         _check_inputs(q, o_low)
     if seq_lengths is not None:
         _check_lengths(seq_lengths, q)
+    score = _score(softcap, prefix_lengths, q, B)
     if (alibi_slopes is None and key_padding is None and o_low is None and dropout is None
-            and not fused and seq_lengths is None and cu_seqlens is None):
+            and not fused and seq_lengths is None and cu_seqlens is None and score is None):
         fa_bwd(q, k, v, o, do, lse, dq, dk, dv, ws, scale, causal, window, stream)
     else:
         opt = options(alibi_slopes, key_padding, o_low, *(dropout or ()),
                       fused=fused, seq_lengths=seq_lengths, cu_seqlens=cu_seqlens,
                       total_tokens=total)
-        fa_bwd_ex(q, k, v, o, do, lse, dq, dk, dv, ws, opt, scale, causal, window, stream,
-                  dims=(B, H, N, d))
+        if score is None:
+            fa_bwd_ex(q, k, v, o, do, lse, dq, dk, dv, ws, opt, scale, causal, window, stream,
+                      dims=(B, H, N, d))
+        else:
+            fa_bwd_score(q, k, v, o, do, lse, dq, dk, dv, ws, opt, score, scale, causal, window,
+                         stream, dims=(B, H, N, d))
     return dq, dk, dv
 
 

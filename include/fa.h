@@ -205,6 +205,31 @@ fa_status_t fa_fwd_fp8(const void *q, const void *k, const void *v, float q_scal
                        int d, float scale, int causal, fa_window_t window, void *stream);
 
 /*
+ * Changes to the scores before the softmax, for fa_fwd_score and fa_bwd_score. (The pages have
+ * no counterpart; an interface addition of this library.) A null pointer, or a zero-initialised
+ * struct, means none.
+ *
+ *   prefix_lengths  B int32, device memory, 4-byte aligned, or NULL: key j of sequence b is
+ *            visible from query i iff j <= i or j < prefix_lengths[b] (a prompt or an image that
+ *            is seen in both directions, followed by causal tokens). Values are clamped to
+ *            [0, real length]. For causal problems (else FA_ERR_INVALID_ARG) without a left
+ *            window (else FA_ERR_UNSUPPORTED).
+ *   softcap  c > 0 caps the scaled scores s: they become c tanh(s / c), before an ALiBi bias, the
+ *            mask and the softmax (LSE is that of the capped scores); 0 = no cap. Finite, >= 0,
+ *            and c, scale / c and its inverse ordinary fp32 numbers (else FA_ERR_INVALID_ARG).
+ */
+typedef struct {
+    const int *prefix_lengths;
+    float softcap;
+} fa_score_t;
+
+/* fa_fwd_ex with `score` (may be NULL). */
+fa_status_t fa_fwd_score(const void *q, const void *k, const void *v, void *o, float *lse,
+                         int B, int H, int N, int d, float scale, int causal,
+                         fa_window_t window, const fa_options_t *options,
+                         const fa_score_t *score, void *stream);
+
+/*
  * Bytes of device workspace fa_bwd() needs: two fp32 arrays of B*H*Np values, where
  * Np = N rounded up to a multiple of 128 (the row statistics of the backward, see
  * fa_bwd_preprocess), rounded up to 256 bytes. Returns 0 for an empty problem or invalid
@@ -255,6 +280,18 @@ fa_status_t fa_bwd_ex(const void *q, const void *k, const void *v, const void *o
                       int B, int H, int N, int d, float scale, int causal,
                       fa_window_t window, const fa_options_t *options, void *workspace,
                       size_t workspace_bytes, void *stream);
+
+/*
+ * fa_bwd_ex with the `score` the forward had (may be NULL): dS gets the factor
+ * 1 - tanh(s / c)^2 of the cap. The workspace is that of fa_bwd_workspace_bytes_ex with the same
+ * options. Not with FA_BWD_FUSED (FA_ERR_UNSUPPORTED).
+ */
+fa_status_t fa_bwd_score(const void *q, const void *k, const void *v, const void *o,
+                         const void *dout, const float *lse, void *dq, void *dk, void *dv,
+                         int B, int H, int N, int d, float scale, int causal,
+                         fa_window_t window, const fa_options_t *options,
+                         const fa_score_t *score, void *workspace, size_t workspace_bytes,
+                         void *stream);
 
 /*
  * ALiBi: fa_fwd and fa_bwd with a linear bias. Page "告别OOM和训练慢…(含A100环境配置)" §4.2

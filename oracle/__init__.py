@@ -52,11 +52,11 @@ class Oracle:
         lp = ctypes.POINTER(ctypes.c_long)
         self.lib.oracle_attention_fwd.argtypes = [
             _dptr, _dptr, _dptr, L, L, L, L, D, ctypes.c_int, L, L, _dptr, _bptr, lp, D, U64,
-            U64, _dptr, _dptr]
+            U64, D, lp, _dptr, _dptr]
         self.lib.oracle_attention_fwd.restype = ctypes.c_int
         self.lib.oracle_attention_bwd.argtypes = [
             _dptr, _dptr, _dptr, _dptr, L, L, L, L, D, ctypes.c_int, L, L, _dptr, _bptr, lp, D,
-            U64, U64, _dptr, _dptr, _dptr]
+            U64, U64, D, lp, _dptr, _dptr, _dptr]
         self.lib.oracle_attention_bwd.restype = ctypes.c_int
         u32p = ctypes.POINTER(ctypes.c_uint32)
         self.lib.oracle_philox4x32_10.argtypes = [u32p, u32p, u32p]
@@ -128,10 +128,11 @@ class Oracle:
         return m
 
     def fwd(self, q, k, v, scale, causal=False, window=(-1, -1), alibi=None, key_padding=None,
-            dropout=None, lengths=None):
+            dropout=None, lengths=None, softcap=0.0, prefixes=None):
         """Returns (O, LSE) in fp64 for (B, H, N, d) inputs; `alibi`: H slopes or None;
         `key_padding`: (B, N) flags, True for a padded key, or None; `dropout`:
-        (p, seed, offset) or None; `lengths`: B real lengths or None."""
+        (p, seed, offset) or None; `lengths`: B real lengths or None; `softcap`: a cap of the
+        scores, 0 = none; `prefixes`: B lengths of keys every query sees, or None."""
         q, k, v = self._prep(q, k, v)
         B, H, N, d = q.shape
         o = np.empty_like(q)
@@ -140,16 +141,17 @@ class Oracle:
         keep_pad, pad = self._padding(key_padding, B, N)
         dp, seed, offset = self._dropout(dropout)
         keep_len, lens = self._lengths(lengths, B, N)
+        keep_pre, pre = self._lengths(prefixes, B, N)
         rc = self.lib.oracle_attention_fwd(_as_ptr(q), _as_ptr(k), _as_ptr(v), B, H, N, d,
                                            float(scale), int(bool(causal)), int(window[0]),
                                            int(window[1]), slopes, pad, lens, dp, seed, offset,
-                                           _as_ptr(o), _as_ptr(lse))
+                                           float(softcap), pre, _as_ptr(o), _as_ptr(lse))
         if rc != 0:
             raise RuntimeError("oracle_attention_fwd failed with %d" % rc)
         return o, lse
 
     def bwd(self, q, k, v, do, scale, causal=False, window=(-1, -1), alibi=None,
-            key_padding=None, dropout=None, lengths=None):
+            key_padding=None, dropout=None, lengths=None, softcap=0.0, prefixes=None):
         """Returns (dQ, dK, dV) in fp64: the gradient of <O, dO> for (B, H, N, d) inputs."""
         q, k, v, do = self._prep(q, k, v, do)
         B, H, N, d = q.shape
@@ -160,10 +162,11 @@ class Oracle:
         keep_pad, pad = self._padding(key_padding, B, N)
         dp, seed, offset = self._dropout(dropout)
         keep_len, lens = self._lengths(lengths, B, N)
+        keep_pre, pre = self._lengths(prefixes, B, N)
         rc = self.lib.oracle_attention_bwd(_as_ptr(q), _as_ptr(k), _as_ptr(v), _as_ptr(do),
                                            B, H, N, d, float(scale), int(bool(causal)),
                                            int(window[0]), int(window[1]), slopes, pad, lens,
-                                           dp, seed, offset, _as_ptr(dq), _as_ptr(dk),
+                                           dp, seed, offset, float(softcap), pre, _as_ptr(dq), _as_ptr(dk),
                                            _as_ptr(dv))
         if rc != 0:
             raise RuntimeError("oracle_attention_bwd failed with %d" % rc)

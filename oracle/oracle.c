@@ -57,6 +57,10 @@
  *     weights are scaled by 256 / (256 - t), i.e. by 1 / (1 - p') with p' = t / 256 the
  *     probability the generator really drops with (p is rounded to a multiple of 1/256).
  *
+ * Capped scores and prefixes (no counterpart on the pages): with a cap c > 0 the scaled score s
+ * becomes c tanh(s / c) before the bias and the mask, so that dS = P o (dP - D) o (1 - tanh^2);
+ * with prefix lengths p_b, query i of batch entry b also sees every key j < p_b (i, j < L_b).
+ *
  * Readings where the pages are silent:
  *   - visible(i, j) <=> (left < 0 or j >= i - left) and (right < 0 or j <= i + right);
  *     -1 means unbounded; causal forces right = min(right, 0) (right = 0 when unbounded).
@@ -86,8 +90,9 @@ static int resolve_right(int causal, long right)
     return (int)right;
 }
 
-static int visible(long i, long j, long left, long right)
+static int visible(long i, long j, long left, long right, long prefix)
 {
+    if (j < prefix) return 1;
     if (left >= 0 && j < i - left) return 0;
     if (right >= 0 && j > i + right) return 0;
     return 1;
@@ -101,10 +106,12 @@ static double head_slope(const double *alibi_slopes, long bh, long H)
 
 /* P (N x N) := softmax rows of the masked, scaled (and biased, when slope != 0) scores of
  * one head; lse (N). kpad: N flags of the head's batch entry (nonzero = padded key), or
- * NULL; len: the entry's real length (N when the batch is not variable-length). */
+ * NULL; len: the entry's real length (N when the batch is not variable-length); cap: 0 = none;
+ * prefix: keys every query sees; G (N x N, or NULL): the cap's derivative at each score. */
 static void head_probabilities(const double *q, const double *k, long N, long d,
                                double scale, double slope, long left, long right,
-                               const unsigned char *kpad, long len, double *P, double *lse)
+                               const unsigned char *kpad, long len, double cap, long prefix,
+                               double *P, double *lse, double *G)
 {
     long i;
 #pragma omp parallel for schedule(static)
@@ -116,8 +123,10 @@ static void head_probabilities(const double *q, const double *k, long N, long d,
             double s = 0.0;
             for (c = 0; c < d; ++c) s += q[i * d + c] * k[j * d + c];
             s *= scale;
+            if (G) G[i * N + j] = cap > 0.0 ? 1.0 - tanh(s / cap) * tanh(s / cap) : 1.0;
+            if (cap > 0.0) s = cap * tanh(s / cap);
             s += -slope * fabs((double)(i - j));
-            if (!visible(i, j, left, right)) s = -INFINITY;
+            if (!visible(i, j, left, right, prefix)) s = -INFINITY;
             if (kpad && kpad[j]) s = -INFINITY;
             if (i >= len || j >= len) s = -INFINITY;
             Pi[j] = s;
@@ -224,6 +233,12 @@ static long head_length(const long *lengths, long bh, long H, long N)
     return lengths ? lengths[bh / H] : N;
 }
 
+/* The prefix of head bh's batch entry: prefixes[b], or 0 without prefixes. */
+static long head_prefix(const long *prefixes, long bh, long H)
+{
+    return prefixes ? prefixes[bh / H] : 0;
+}
+
 /* The key-padding flags of head bh's batch entry (B*H heads, heads fastest), or NULL. */
 static const unsigned char *head_padding(const unsigned char *key_padding, long bh, long H,
                                          long N)
@@ -233,13 +248,13 @@ static const unsigned char *head_padding(const unsigned char *key_padding, long 
 
 /* alibi_slopes: H slopes, or NULL for no bias; key_padding: B x N flags (nonzero = padded
  * key), or NULL for none; lengths: B real lengths in [0, N], or NULL; dropout_p in [0, 1),
- * 0 for none, with its seed and offset. */
+ * 0 for none, with its seed and offset; softcap: 0 for none; prefixes: B lengths, or NULL. */
 int oracle_attention_fwd(const double *q, const double *k, const double *v,
                          long B, long H, long N, long d, double scale,
                          int causal, long left, long right, const double *alibi_slopes,
                          const unsigned char *key_padding, const long *lengths,
                          double dropout_p, unsigned long long seed, unsigned long long offset,
-                         double *o, double *lse)
+                         double softcap, const long *prefixes, double *o, double *lse)
 {
     long bh;
     if (B < 0 || H < 0 || N < 0 || d < 1) return 1;
@@ -253,7 +268,8 @@ int oracle_attention_fwd(const double *q, const double *k, const double *v,
         long i;
         head_probabilities(qh, kh, N, d, scale, head_slope(alibi_slopes, bh, H), left, right,
                            head_padding(key_padding, bh, H, N),
-                           head_length(lengths, bh, H, N), P, lse + bh * N);
+                           head_length(lengths, bh, H, N), softcap,
+                           head_prefix(prefixes, bh, H), P, lse + bh * N, NULL);
         apply_dropout(P, N, bh, dropout_p, seed, offset);
         /* O = P V (P with dropout applied) */
 #pragma omp parallel for schedule(static)
@@ -276,7 +292,7 @@ int oracle_attention_bwd(const double *q, const double *k, const double *v,
                          int causal, long left, long right, const double *alibi_slopes,
                          const unsigned char *key_padding, const long *lengths,
                          double dropout_p, unsigned long long seed, unsigned long long offset,
-                         double *dq, double *dk, double *dv)
+                         double softcap, const long *prefixes, double *dq, double *dk, double *dv)
 {
     long bh;
     if (B < 0 || H < 0 || N < 0 || d < 1) return 1;
@@ -288,10 +304,11 @@ int oracle_attention_bwd(const double *q, const double *k, const double *v,
     double *P = (double *)malloc(sizeof(double) * nn);
     double *Pd = (double *)malloc(sizeof(double) * nn);
     double *dP = (double *)malloc(sizeof(double) * nn);
+    double *G = (double *)malloc(sizeof(double) * nn);
     double *lse = (double *)malloc(sizeof(double) * (size_t)(N > 0 ? N : 1));
     double *D = (double *)malloc(sizeof(double) * (size_t)(N > 0 ? N : 1));
-    if (!P || !Pd || !dP || !lse || !D) {
-        free(P); free(Pd); free(dP); free(lse); free(D);
+    if (!P || !Pd || !dP || !G || !lse || !D) {
+        free(P); free(Pd); free(dP); free(G); free(lse); free(D);
         return 2;
     }
     for (bh = 0; bh < B * H; ++bh) {
@@ -301,7 +318,8 @@ int oracle_attention_bwd(const double *q, const double *k, const double *v,
         long i, j;
         head_probabilities(qh, kh, N, d, scale, head_slope(alibi_slopes, bh, H), left, right,
                            head_padding(key_padding, bh, H, N),
-                           head_length(lengths, bh, H, N), P, lse);
+                           head_length(lengths, bh, H, N), softcap,
+                           head_prefix(prefixes, bh, H), P, lse, G);
         /* Pd = P o Z / (1 - p'): the weights that multiplied V (Pd = P without dropout) */
         memcpy(Pd, P, sizeof(double) * (size_t)N * (size_t)N);
         apply_dropout(Pd, N, bh, dropout_p, seed, offset);
@@ -330,6 +348,7 @@ int oracle_attention_bwd(const double *q, const double *k, const double *v,
             }
             D[i] = acc;
             for (jj = 0; jj < N; ++jj) dP[i * N + jj] = P[i * N + jj] * (dP[i * N + jj] - D[i]);
+            for (jj = 0; jj < N; ++jj) dP[i * N + jj] *= G[i * N + jj];
         }
         /* dQ = scale * dS K */
 #pragma omp parallel for schedule(static)
@@ -354,7 +373,7 @@ int oracle_attention_bwd(const double *q, const double *k, const double *v,
             for (c = 0; c < d; ++c) dkh[j * d + c] *= scale;
         }
     }
-    free(P); free(Pd); free(dP); free(lse); free(D);
+    free(P); free(Pd); free(dP); free(G); free(lse); free(D);
     return 0;
 }
 

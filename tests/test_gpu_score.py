@@ -1,0 +1,358 @@
+"""Capped scores and prefixes on the GPU against the fp64 oracle.
+
+Tolerances: those of the plain attention (gpu_helpers), whose arithmetic is the same: P, dS and
+the outputs are rounded to bf16 (relative error up to 2^-8 each, 2^-8 / sqrt(3) in the norm), and
+the cap adds an fp32 tanh: in the polynomial 1.1e-7 relative, in the exact form 1 - 2 / (1 + e^2u)
+an absolute error below 4e-7, so a score is off by at most 4e-7 c, LSE by as much: 1e-3 holds up to
+c = 2500, where no score of these inputs leaves the polynomial's range. Gradients with a cap can
+be small where most scores sit on it (1 - tanh^2); the error of 1 - tanh^2 is below 1e-6, far
+below the bf16 rounding of what remains unless the factor itself is below 1e-4."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from exact_attention_126_b200 import fa, synth
+from gpu_helpers import (assert_within_bounds, cumulative, ensure_built, pack_rows, rel_frob)
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    ensure_built()
+
+
+def inputs(B, H, N, d, seed=0, spread=1.0):
+    g = torch.Generator().manual_seed(1000 + seed)
+    t = {n: torch.randn(B, H, N, d, generator=g) for n in ("q", "k", "v", "do")}
+    t["q"] = t["q"] * spread
+    return {n: x.to(BF16) for n, x in t.items()}
+
+
+def run(inp, scale, causal, window=(-1, -1), softcap=0.0, prefixes=None, lengths=None,
+        packed=False, alibi=None, key_padding=None, dropout=None, residual=True):
+    dev = torch.device("cuda:0")
+    B, H, N, d = inp["q"].shape
+    i32 = lambda x: None if x is None else torch.tensor(x, dtype=torch.int32, device=dev)  # noqa
+    kw = dict(scale=scale, causal=causal, window=window, softcap=softcap,
+              prefix_lengths=i32(prefixes),
+              alibi_slopes=None if alibi is None else torch.tensor(alibi, device=dev),
+              key_padding=None if key_padding is None else key_padding.to(dev), dropout=dropout)
+    t = {n: (pack_rows(x, lengths) if packed else x).to(dev) for n, x in inp.items()}
+    if packed:
+        kw.update(cu_seqlens=i32(cumulative(lengths)), max_seqlen=N)
+    else:
+        kw["seq_lengths"] = i32(lengths)
+    res = fa.attention_forward(t["q"], t["k"], t["v"], keep_residual=residual, **kw)
+    o, lse = res[:2]
+    dq, dk, dv = fa.attention_backward(t["q"], t["k"], t["v"], o, lse, t["do"],
+                                       o_low=res[2] if residual else None, **kw)
+    torch.cuda.synchronize()
+    assert fa.fa_debug_status() == 0
+    out = dict(o=o, lse=lse, dq=dq, dk=dk, dv=dv)
+    if packed:
+        c = cumulative(lengths)
+        full = {}
+        for n, x in out.items():
+            y = torch.full((B, H, N), float("-inf")) if n == "lse" else torch.zeros(B, H, N, d)
+            for b, L in enumerate(lengths):
+                y[b, :, :L] = (x[:, c[b]:c[b] + L] if n == "lse"
+                               else x[c[b]:c[b] + L].transpose(0, 1)).float().cpu()
+            full[n] = y
+        out = full
+    return {n: x.float().cpu() for n, x in out.items()}
+
+
+def errors(inp, out, scale, causal, window=(-1, -1), softcap=0.0, prefixes=None, lengths=None,
+           alibi=None, key_padding=None, dropout=None):
+    f = {n: synth.to_f64(x) for n, x in inp.items()}
+    N = inp["q"].shape[2]
+    clip = lambda x: None if x is None else np.clip(x, 0, N)  # noqa
+    kp = None if key_padding is None else key_padding.numpy().astype(np.uint8)
+    kw = dict(alibi=alibi, key_padding=kp, dropout=dropout, lengths=clip(lengths),
+              softcap=softcap, prefixes=clip(prefixes))
+    o, lse = oracle.fwd(f["q"], f["k"], f["v"], scale, causal, window, **kw)
+    g = oracle.bwd(f["q"], f["k"], f["v"], f["do"], scale, causal, window, **kw)
+    got = {n: x.double().numpy() for n, x in out.items()}
+    dead = np.isneginf(lse)
+    assert np.array_equal(np.isneginf(got["lse"]), dead)
+    assert (got["o"][dead] == 0).all() and (got["dq"][dead] == 0).all()
+    e = {"o": rel_frob(got["o"], o),
+         "lse": float(np.abs(got["lse"][~dead] - lse[~dead]).max()) if (~dead).any() else 0.0}
+    for n, r in zip(("dq", "dk", "dv"), g):
+        e[n] = rel_frob(got[n], r)
+    return e
+
+
+def check(inp, scale, causal, window=(-1, -1), packed=False, residual=True, **kw):
+    out = run(inp, scale, causal, window, packed=packed, residual=residual, **kw)
+    assert_within_bounds(errors(inp, out, scale, causal, window, **kw), (causal, window, kw))
+    return out
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N", [2, 17, 128, 129, 300])
+@pytest.mark.parametrize("causal,window", [(False, (-1, -1)), (True, (-1, -1)),
+                                           (False, (40, 11)), (True, (33, 0))])
+@pytest.mark.parametrize("cap", [50.0, 2.0])
+def test_cap(d, N, causal, window, cap):
+    check(inputs(2, 2, N, d, N, spread=2.0), 0.125, causal, window, softcap=cap)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap", [0.05, 0.5, 7.0, 300.0, 2000.0])
+def test_cap_sizes(d, cap):
+    """From caps that hold every score to caps that hold none, rows on either side of the
+    polynomial's range in one warp."""
+    inp = inputs(1, 2, 200, d, 3, spread=3.0)
+    inp["q"][:, :, ::7] *= 5
+    check(inp, 0.2, False, softcap=cap)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_saturated_scores(d):
+    """Scores far past the cap: finite outputs, and gradients of exactly zero where 1 - tanh^2
+    rounds to zero."""
+    inp = inputs(1, 1, 130, d, 5)
+    inp["q"] = torch.full_like(inp["q"], 64.0)
+    inp["k"] = torch.full_like(inp["k"], 64.0)
+    inp["k"][:, :, ::2] *= -1
+    out = run(inp, 1.0, False, softcap=3.0)
+    f = {n: synth.to_f64(x) for n, x in inp.items()}
+    o, lse = oracle.fwd(f["q"], f["k"], f["v"], 1.0, softcap=3.0)
+    assert rel_frob(out["o"].double().numpy(), o) < 5e-3
+    assert np.abs(out["lse"].double().numpy() - lse).max() < 1e-3
+    assert (out["dq"] == 0).all() and (out["dk"] == 0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap", [0.0, 10.0])
+@pytest.mark.parametrize("N", [1, 127, 128, 129, 500])
+def test_prefix(d, cap, N):
+    pre = [0, 1, N // 2, N - 1, N, N + 50, -3, 128]
+    if N == 1:  # one key: its gradients with respect to q and k are zero
+        out = run(inputs(8, 1, 1, d), 0.125, True, softcap=cap, prefixes=pre)
+        assert np.abs(out["dq"].numpy()).max() < 1e-3
+        assert np.abs(out["o"].numpy() - inputs(8, 1, 1, d)["v"].float().numpy()).max() < 1e-6
+        return
+    check(inputs(8, 1, N, d, N), 0.125, True, softcap=cap, prefixes=pre)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("cap", [0.0, 10.0])
+def test_prefix_lengths(d, packed, cap):
+    lens = [300, 0, 1, 129, 255, 256]
+    pre = [140, 5, 1, 300, 0, 200]
+    check(inputs(6, 2, 300, d, 9), 0.125, True, packed=packed, softcap=cap, prefixes=pre,
+          lengths=lens)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("packed", [False, True])
+def test_every_option_at_once(d, packed):
+    B, H, N = 4, 3, 270
+    lens = [270, 64, 200, 129]
+    g = torch.Generator().manual_seed(3)
+    pad = torch.rand(B, N, generator=g) < 0.2
+    pad[1] = True  # an entry without a visible key
+    check(inputs(B, H, N, d, 11, spread=2.0), 0.125, True, packed=packed, softcap=5.0,
+          prefixes=[100, 64, 0, 129], lengths=lens, alibi=[0.5, 0.1, 0.02], key_padding=pad,
+          dropout=(0.2, 1234, 5))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("opt", ["alibi", "pad", "dropout"])
+def test_each_option(d, opt):
+    g = torch.Generator().manual_seed(4)
+    kw = {"alibi": dict(alibi=[0.3, 0.01]), "pad": dict(key_padding=torch.rand(2, 260,
+                                                                              generator=g) < 0.4),
+          "dropout": dict(dropout=(0.1, 77, 1))}[opt]
+    inp = inputs(2, 2, 260, d, 12, spread=2.0)
+    check(inp, 0.125, False, softcap=8.0, **kw)
+    check(inp, 0.125, True, softcap=8.0, prefixes=[130, 31], residual=False, **kw)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_items_per_sm(d):
+    """More tiles than SMs, with even and odd tile counts (the paired and chunked schedules);
+    sampled heads against the oracle."""
+    for N in (1024, 900):
+        B, H = 6, 8
+        inp = inputs(B, H, N, d, 13)
+        pre = [0, 1000, 129, 512, 700, 3]
+        out = run(inp, 0.125, True, softcap=6.0, prefixes=pre)
+        for b, h in ((0, 0), (1, 3), (3, 5), (5, 7)):
+            one = {n: x[b:b + 1, h:h + 1] for n, x in inp.items()}
+            got = {n: x[b:b + 1, h:h + 1] for n, x in out.items()}
+            assert_within_bounds(errors(one, got, 0.125, True, softcap=6.0, prefixes=[pre[b]]),
+                                 (N, b, h))
+
+
+def test_no_cap_and_no_prefix_is_the_plain_call():
+    dev = torch.device("cuda:0")
+    inp = inputs(2, 2, 200, 64)
+    q, k, v = (inp[n].to(dev) for n in "qkv")
+    a = fa.attention_forward(q, k, v, causal=True)
+    b = fa.attention_forward(q, k, v, causal=True, softcap=0.0, prefix_lengths=None)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    # prefixes of no keys: the causal result, through the other kernels
+    z = torch.zeros(2, dtype=torch.int32, device=dev)
+    c = fa.attention_forward(q, k, v, causal=True, prefix_lengths=z)
+    assert all(torch.equal(x, y) for x, y in zip(a, c))
+
+
+def test_packed_equals_padded():
+    lens, pre = [130, 70, 256], [60, 70, 0]
+    inp = inputs(3, 2, 256, 128, 14)
+    a = run(inp, 0.1, True, softcap=4.0, prefixes=pre, lengths=lens)
+    b = run(inp, 0.1, True, softcap=4.0, prefixes=pre, lengths=lens, packed=True)
+    assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+def test_repeats_streams_and_graphs():
+    dev = torch.device("cuda:0")
+    inp = {n: x.to(dev) for n, x in inputs(2, 4, 700, 64, 15).items()}
+    pre = torch.tensor([300, 0], dtype=torch.int32, device=dev)
+    kw = dict(causal=True, softcap=9.0, prefix_lengths=pre)
+
+    def step(stream=None):
+        o, lse, low = fa.attention_forward(inp["q"], inp["k"], inp["v"], keep_residual=True,
+                                           stream=stream, **kw)
+        return (o, lse) + fa.attention_backward(inp["q"], inp["k"], inp["v"], o, lse, inp["do"],
+                                                o_low=low, stream=stream, **kw)
+
+    ref = step()
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    runs = []
+    for _ in range(6):
+        for s in (s1, s2):
+            with torch.cuda.stream(s):
+                runs.append(step())
+    runs.append(step(s1))
+    torch.cuda.synchronize()
+    for r in runs:
+        assert all(torch.equal(a, b) for a, b in zip(r, ref))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for t in out:
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, ref))
+
+
+def test_packed_rows_outside_are_left_alone():
+    dev = torch.device("cuda:0")
+    total, H, d = 400, 2, 64
+    cu = torch.tensor([20, 150, 150, 380], dtype=torch.int32, device=dev)
+    pre = torch.tensor([40, 9, 500], dtype=torch.int32, device=dev)
+    q, k, v, do = (torch.randn(total, H, d, device=dev).to(BF16) for _ in range(4))
+    dims = (3, H, 230, d)
+    opt = fa.options(cu_seqlens=cu, total_tokens=total)
+    score = fa.fa_score_t(pre.data_ptr(), 7.0)
+    o, dq, dk, dv = (torch.full_like(q, 5.0) for _ in range(4))
+    lse = torch.full((H, total), 5.0, device=dev)
+    ws = torch.empty(fa.fa_bwd_workspace_bytes_ex(*dims, opt), dtype=torch.uint8, device=dev)
+    fa.fa_fwd_score(q, k, v, o, lse, opt, score, causal=True, dims=dims)
+    fa.fa_bwd_score(q, k, v, o, do, lse, dq, dk, dv, ws, opt, score, causal=True, dims=dims)
+    torch.cuda.synchronize()
+    assert fa.fa_debug_status() == 0
+    for t in (o, dq, dk, dv):
+        assert (t[:20] == 5.0).all() and (t[380:] == 5.0).all()
+        assert torch.isfinite(t.float()).all() and not (t[20:380] == 5.0).all(-1).any()
+    assert (lse[:, :20] == 5.0).all() and (lse[:, 380:] == 5.0).all()
+
+
+def test_refusals():
+    dev = torch.device("cuda:0")
+    q = torch.randn(2, 2, 130, 64, device=dev).to(BF16)
+    pre = torch.zeros(2, dtype=torch.int32, device=dev)
+    for bad in (pre.long(), pre.cpu(), pre[:1], torch.zeros(4, dtype=torch.int32,
+                                                            device=dev)[::2]):
+        with pytest.raises(ValueError):
+            fa.attention_forward(q, q, q, causal=True, prefix_lengths=bad)
+    for kw in (dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=float("inf")),
+               dict(softcap=1e-44), dict(prefix_lengths=pre),
+               dict(prefix_lengths=pre, causal=True, window=(5, 0))):
+        with pytest.raises(fa.FAError):
+            fa.attention_forward(q, q, q, **kw)
+    with pytest.raises(fa.FAError):
+        fa.attention_backward(q, q, q, q, torch.zeros(2, 2, 130, device=dev), q, softcap=3.0,
+                              fused=True)
+    assert ctypes.sizeof(fa.fa_score_t) == 16
+
+
+@pytest.mark.parametrize("d,interleaved", [(64, False), (128, True)])
+@pytest.mark.parametrize("packed", [False, True])
+def test_layer(d, interleaved, packed):
+    """A layer's path as it is trained: projection -> norm and rotation -> capped attention with
+    prefixes -> gradients -> projection, against the same in 64 bits."""
+    import rope_ref
+    dev = torch.device("cuda:0")
+    B, N, H, cap, eps = 3, 200, 2, 6.0, 1e-6
+    lens = [200, 77, 130]
+    pre = [50, 77, 0]
+    g = torch.Generator().manual_seed(21)
+    qkv = torch.randn(B, N, 3 * H, d, generator=g).to(BF16)
+    do = torch.randn(B, H, N, d, generator=g).to(BF16)
+    gains = [1 + 0.2 * torch.randn(d, generator=g) for _ in range(2)]
+    freq = (10000.0 ** (-torch.arange(d // 2, dtype=torch.float64) / (d // 2))).float()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)  # noqa
+    if packed:
+        x = torch.cat([qkv[b, :n] for b, n in enumerate(lens)]).to(dev)
+        dox = pack_rows(do, lens).to(dev)
+        lay = dict(cu_seqlens=i32(cumulative(lens)), max_seqlen=N)
+    else:
+        x, dox, lay = qkv.to(dev), do.to(dev), dict(seq_lengths=i32(lens))
+    rope = dict(q_weight=gains[0].to(dev), k_weight=gains[1].to(dev), eps=eps,
+                inv_freq=freq.to(dev), interleaved=interleaved, **lay)
+    att = dict(causal=True, softcap=cap, prefix_lengths=i32(pre), **lay)
+    xq, xk, xv = x.split(H, -2)
+    q, k, v = fa.qk_norm_rope_forward(xq, xk, xv, **rope)
+    o, lse, low = fa.attention_forward(q, k, v, keep_residual=True, **att)
+    dq, dk, dv = fa.attention_backward(q, k, v, o, lse, dox, o_low=low, **att)
+    dx = torch.empty_like(x)
+    grads = fa.qk_norm_rope_backward(dq, dk, dv, xq, xk, out=dx.split(H, -2), **rope)
+    torch.cuda.synchronize()
+    # 64 bits, with Q and K rounded to bf16 where the path rounds them
+    f = lambda t: t.double().numpy()  # noqa
+    ang = rope_ref.angles(np.arange(N)[None], f(freq), None)
+    out = [np.zeros((B, N, H, d)) for _ in range(3)]
+    dg = [0.0, 0.0]
+    scale = 1 / np.sqrt(d)
+    for b, n in enumerate(lens):
+        src = [f(t) for t in qkv[b, :n].split(H, 1)]
+        y = [rope_ref.forward(src[i], f(gains[i]), ang[:n], interleaved, True, eps)
+             for i in range(2)]
+        y = [f(torch.tensor(t).to(BF16)).transpose(1, 0, 2)[None] for t in y]
+        vv = src[2].transpose(1, 0, 2)[None]
+        kw = dict(softcap=cap, prefixes=[min(pre[b], n)])
+        gr = oracle.bwd(y[0], y[1], vv, f(do[b:b + 1, :, :n]), scale, True, **kw)
+        ro, rl = oracle.fwd(y[0], y[1], vv, scale, True, **kw)
+        c = cumulative(lens)[b]
+        go = o[c:c + n].transpose(0, 1) if packed else o[b, :, :n]
+        assert rel_frob(f(go.cpu()), ro[0]) < 5e-3
+        for i in range(2):
+            gx, gg, _ = rope_ref.backward(gr[i][0].transpose(1, 0, 2), src[i], f(gains[i]),
+                                          ang[:n], interleaved, True, eps)
+            out[i][b, :n] = gx
+            dg[i] = dg[i] + gg
+        out[2][b, :n] = gr[2][0].transpose(1, 0, 2)
+    for i, t in enumerate(dx.split(H, -2)):
+        t = f(t.cpu())
+        if packed:
+            full = np.zeros((B, N, H, d))
+            for b, n in enumerate(lens):
+                full[b, :n] = t[cumulative(lens)[b]:cumulative(lens)[b] + n]
+            t = full
+        # the attention's gradient is within 1e-2; the norm's and the last rounding add 2^-8
+        assert rel_frob(t, out[i]) < 1e-2 + 2.0 ** -8, i
+    for i in range(2):
+        assert rel_frob(f(grads[3 + i].cpu()), dg[i]) < 1e-2 + 2.0 ** -8
