@@ -509,6 +509,13 @@ fa_status_t resolve_rows(const fa_heads_t* h, int B, int N, int d, bool packed, 
     if (x.stride % 8 != 0) return FA_ERR_MISALIGNED;
   }
   if (!aligned16(h->data)) return FA_ERR_MISALIGNED;
+  // the kernels step through a kind's rows in 32-bit counts of 8 bytes
+  long long reach = d;
+  for (const Dim& x : dims) {
+    if (x.stride > 0 && x.extent - 1 >= (1ll << 34) / x.stride) return FA_ERR_UNSUPPORTED;
+    reach += (x.extent - 1) * x.stride;
+  }
+  if (reach >= (1ll << 34)) return FA_ERR_UNSUPPORTED;
   if (written) {
     for (int i = 0; i < 2; ++i)
       for (int j = 0; j < 2 - i; ++j)
@@ -539,7 +546,7 @@ fa_status_t resolve_rope(int B, int N, int d, const fa_norm_rope_t* p, fa::RopeA
     return FA_ERR_INVALID_ARG;
   }
   if (p->rotary_dim < 0) return FA_ERR_INVALID_ARG;
-  if (p->rotary_dim > d || p->rotary_dim % 16 != 0) return FA_ERR_UNSUPPORTED;
+  if (p->rotary_dim > d || p->rotary_dim % 8 != 0) return FA_ERR_UNSUPPORTED;
   if (p->rotary_dim > 0) {
     if (p->inv_freq == nullptr || p->axes < 1) return FA_ERR_INVALID_ARG;
     if (p->axes > FA_MAX_AXES) return FA_ERR_UNSUPPORTED;

@@ -15,13 +15,13 @@
 //   dx = r (w o g - x^ mean(w o g o x^)).
 //
 // Both kernels are bound by device memory: each value is read and written once (the backward
-// reads dy and x). A warp owns one token (or a share of its rows when there are few tokens),
-// so the cosines and sines of the token are computed once, by the warp's lanes side by side,
-// and serve all of its heads. A row is spread over D / 16 lanes, 16 values (two 16-byte
-// vectors) each, chosen so that both members of every pair sit in one lane: lane c holds
-// values 16c .. 16c+15 of an interleaved row, and of a row with split halves values
-// 8c .. 8c+7 of either half. The row sums of the norm then take log2(D / 16) shuffles, and
-// several rows per warp are in flight before the first is used.
+// reads dy and x). A row is spread over D / 8 lanes, eight values each, chosen so that both
+// members of every pair sit in one lane: lane c holds values 8c .. 8c+7 of an interleaved row,
+// and of a row with split halves values 4c .. 4c+3 of either half. A warp covers 32 / (D / 8)
+// rows at once (a unit) and owns one token (or a share of its units when tokens are few): the
+// cosines and sines of the token are computed once, by the lanes side by side, and serve all of
+// its heads. Units go in batches, queries first, then keys, then values; the loads of a batch are
+// issued before the previous one is worked on.
 //
 // Angles. Positions reach 2^31 and the fp32 product pos * inv_freq would lose the angle
 // itself (at position 2^20 its rounding error is 0.06 radians). The frequency is therefore
@@ -38,13 +38,13 @@
 
 namespace fa {
 
-// One token as a warp sees it.
+// One token: where its rows lie and whether it takes part.
 struct RopeToken {
   int b;
   int n;       // row: n of entry b, or packed: the token's index
   int place;   // place in its sequence
   bool live;   // within its sequence's real length
-  bool owned;  // a row the call writes (packed: some sequence covers it)
+  bool owned;  // its rows are written (packed: some sequence covers it)
 };
 
 __device__ __forceinline__ RopeToken rope_token(const RopeArgs& a, int t) {
@@ -53,8 +53,8 @@ __device__ __forceinline__ RopeToken rope_token(const RopeArgs& a, int t) {
     k.b = t / a.N;
     k.n = t - k.b * a.N;
     k.place = k.n;
-    k.owned = true;
-    k.live = a.seq_len == nullptr || k.n < __ldg(a.seq_len + k.b);
+    k.owned = t < a.tokens;
+    k.live = k.owned && (a.seq_len == nullptr || k.n < __ldg(a.seq_len + k.b));
     return k;
   }
   // the last sequence that starts at or before t (empty ones before it are passed over)
@@ -68,89 +68,80 @@ __device__ __forceinline__ RopeToken rope_token(const RopeArgs& a, int t) {
     }
   }
   const int start = lo < a.B ? __ldg(a.cu + lo) : 0;
-  k.b = lo;
+  k.b = 0;
   k.n = t;
   k.place = t - start;
-  k.owned = k.live = lo < a.B && k.place >= 0 && k.place < a.N;
+  k.owned = k.live = t < a.tokens && lo < a.B && k.place >= 0 && k.place < a.N;
   return k;
 }
 
-// This lane's share of a row: two vectors of eight values at offsets oa and ob, holding the
-// pairs (e[i], f[i]) of rotations 8 * chunk + i when `turns`.
-template <int D>
+// This lane's share of a row: values at offsets oa .. oa+3 and ob .. ob+3, holding the pairs
+// (e[i], f[i]) of rotations 4 * chunk + i when `turns`.
+template <int D, bool kInter>
 struct RopeLane {
-  static constexpr int kLanes = D / 16;      // lanes per row
-  static constexpr int kRows = 32 / kLanes;  // rows a warp covers at once
-  int sub;    // row of the warp's kRows
+  static constexpr int kLanes = D / 8;       // lanes per row
+  static constexpr int kRows = 32 / kLanes;  // rows of a unit
+  int sub;    // row of the unit
   int chunk;  // lane of the row
   int oa, ob;
   bool turns;
 
-  __device__ __forceinline__ RopeLane(const RopeArgs& a, bool interleaved) {
+  __device__ __forceinline__ explicit RopeLane(const RopeArgs& a) {
     const int lane = threadIdx.x & 31;
     sub = lane / kLanes;
     chunk = lane % kLanes;
-    turns = 16 * chunk < a.rot;
-    const bool split = turns && !interleaved;
-    oa = split ? 8 * chunk : 16 * chunk;
-    ob = split ? a.rot / 2 + 8 * chunk : 16 * chunk + 8;
+    turns = 8 * chunk < a.rot;
+    const bool split = turns && !kInter;
+    oa = split ? 4 * chunk : 8 * chunk;
+    ob = split ? a.rot / 2 + 4 * chunk : 8 * chunk + 4;
   }
+  // the column of member i (0 .. 3) of this lane's e and f
+  __device__ __forceinline__ int col_e(int i) const { return kInter ? oa + 2 * i : oa + i; }
+  __device__ __forceinline__ int col_f(int i) const { return kInter ? oa + 2 * i + 1 : ob + i; }
 };
 
-// The sixteen values of a lane: first and second members of its eight pairs.
+// A lane's eight values as they lie in memory.
+struct RopeRaw {
+  uint2 a, b;
+};
+
+// The eight values: first and second members of four pairs, two pairs per element.
 struct Pairs {
-  float e[8], f[8];
+  float2 e[2], f[2];
 };
 
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 template <bool kInter>
-__device__ __forceinline__ void unpack_pairs(const uint4& a, const uint4& b, Pairs& p) {
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (kInter) {
-      p.e[i] = bf_lo(w[i]);
-      p.f[i] = bf_hi(w[i]);
-    } else {
-      p.e[i] = (i & 1) ? bf_hi(w[i / 2]) : bf_lo(w[i / 2]);
-      p.f[i] = (i & 1) ? bf_hi(w[4 + i / 2]) : bf_lo(w[4 + i / 2]);
-    }
+__device__ __forceinline__ Pairs unpack_pairs(const RopeRaw& r) {
+  Pairs p;
+  if (kInter) {
+    p.e[0] = make_float2(bf_lo(r.a.x), bf_lo(r.a.y));
+    p.f[0] = make_float2(bf_hi(r.a.x), bf_hi(r.a.y));
+    p.e[1] = make_float2(bf_lo(r.b.x), bf_lo(r.b.y));
+    p.f[1] = make_float2(bf_hi(r.b.x), bf_hi(r.b.y));
+  } else {
+    p.e[0] = make_float2(bf_lo(r.a.x), bf_hi(r.a.x));
+    p.e[1] = make_float2(bf_lo(r.a.y), bf_hi(r.a.y));
+    p.f[0] = make_float2(bf_lo(r.b.x), bf_hi(r.b.x));
+    p.f[1] = make_float2(bf_lo(r.b.y), bf_hi(r.b.y));
   }
+  return p;
 }
 
 template <bool kInter>
-__device__ __forceinline__ void pack_pairs(const Pairs& p, uint4& a, uint4& b) {
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (kInter) {
-      w[i] = pack_bf16x2(p.e[i], p.f[i]);
-      w[4 + i] = pack_bf16x2(p.e[4 + i], p.f[4 + i]);
-    } else {
-      w[i] = pack_bf16x2(p.e[2 * i], p.e[2 * i + 1]);
-      w[4 + i] = pack_bf16x2(p.f[2 * i], p.f[2 * i + 1]);
-    }
+__device__ __forceinline__ RopeRaw pack_pairs(const Pairs& p) {
+  RopeRaw r;
+  if (kInter) {
+    r.a = make_uint2(pack_bf16x2(p.e[0].x, p.f[0].x), pack_bf16x2(p.e[0].y, p.f[0].y));
+    r.b = make_uint2(pack_bf16x2(p.e[1].x, p.f[1].x), pack_bf16x2(p.e[1].y, p.f[1].y));
+  } else {
+    r.a = make_uint2(pack_bf16x2(p.e[0].x, p.e[0].y), pack_bf16x2(p.e[1].x, p.e[1].y));
+    r.b = make_uint2(pack_bf16x2(p.f[0].x, p.f[0].y), pack_bf16x2(p.f[1].x, p.f[1].y));
   }
-  a = make_uint4(w[0], w[1], w[2], w[3]);
-  b = make_uint4(w[4], w[5], w[6], w[7]);
-}
-
-// Sixteen fp32 values in the order of unpack_pairs (gains; null = ones).
-template <bool kInter>
-__device__ __forceinline__ void load_gain(const float* w, int oa, int ob, Pairs& p) {
-  float v[16];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[i] = w != nullptr ? __ldg(w + oa + i) : 1.f;
-    v[8 + i] = w != nullptr ? __ldg(w + ob + i) : 1.f;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    p.e[i] = kInter ? v[2 * i] : v[i];
-    p.f[i] = kInter ? v[2 * i + 1] : v[8 + i];
-  }
+  return r;
 }
 
 // The rotations a lane computes for its warp: pairs lane and lane + 32, their frequencies in
@@ -181,9 +172,10 @@ struct RopeTurns {
 
   // Writes the cosine and sine of each of the token's rotations to `cs` (this warp's D / 2
   // entries of shared memory) and loads those of this lane's pairs.
+  template <typename Lane>
   __device__ __forceinline__ void compute(const RopeArgs& a, const RopeToken& k, int t,
-                                          const RopeLane<D>& ln, float2* cs, float (&c)[8],
-                                          float (&s)[8]) const {
+                                          const Lane& ln, float2* cs, float2 (&c)[2],
+                                          float2 (&s)[2]) const {
     if (a.rot == 0) return;
     __syncwarp();  // the previous token's entries have been read
 #pragma unroll
@@ -201,14 +193,12 @@ struct RopeTurns {
     }
     __syncwarp();
     if (ln.turns) {
-      const float4* src = reinterpret_cast<const float4*>(cs + 8 * ln.chunk);
+      const float4* src = reinterpret_cast<const float4*>(cs + 4 * ln.chunk);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         const float4 v = src[i];
-        c[2 * i] = v.x;
-        s[2 * i] = v.y;
-        c[2 * i + 1] = v.z;
-        s[2 * i + 1] = v.w;
+        c[i] = make_float2(v.x, v.z);
+        s[i] = make_float2(v.y, v.w);
       }
     }
   }
@@ -217,227 +207,304 @@ struct RopeTurns {
 template <int D>
 __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
-  for (int off = D / 32; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  for (int off = D / 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
   return v;
 }
 
-__device__ __forceinline__ uint4 ld_vec(const __nv_bfloat16* p) {
-  return *reinterpret_cast<const uint4*>(p);
-}
-__device__ __forceinline__ void st_vec(__nv_bfloat16* p, const uint4& v) {
-  *reinterpret_cast<uint4*>(p) = v;
+// This lane's eight values of the first row it takes of a kind, and of the rows after it: steps of
+// `step` 8-byte units (strides are multiples of 8 values, and a kind's rows span less than 2^34
+// values, checked on the host: 32-bit products do).
+struct RowWalk {
+  const uint2* p;
+  unsigned step;
+  __device__ __forceinline__ const uint2* at(int i) const { return p + (size_t)((unsigned)i * step); }
+};
+__device__ __forceinline__ RowWalk walk_rows(const HeadRows& r, const RopeToken& k, int head,
+                                             int heads_per_step) {
+  return RowWalk{reinterpret_cast<const uint2*>(r.data) +
+                     ((unsigned)k.b * (unsigned)(r.sb >> 2) + (unsigned)k.n * (unsigned)(r.sn >> 2) +
+                      (unsigned)head * (unsigned)(r.sh >> 2)),
+                 (unsigned)heads_per_step * (unsigned)(r.sh >> 2)};
 }
 
-__device__ __forceinline__ __nv_bfloat16* token_rows(const HeadRows& r, const RopeToken& k,
-                                                     bool packed) {
-  return r.data + (packed ? 0 : k.b * r.sb) + k.n * r.sn;
+template <bool kInter, typename Lane>
+__device__ __forceinline__ RopeRaw load_row(const uint2* p, const Lane& ln) {
+  RopeRaw r;
+  if (kInter) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p + 2 * ln.chunk);
+    r.a = make_uint2(v.x, v.y);
+    r.b = make_uint2(v.z, v.w);
+  } else {
+    r.a = p[ln.oa >> 2];
+    r.b = p[ln.ob >> 2];
+  }
+  return r;
+}
+template <bool kInter, typename Lane>
+__device__ __forceinline__ void store_row(const uint2* p, const Lane& ln, const RopeRaw& r) {
+  uint2* q = const_cast<uint2*>(p);
+  if (kInter) {
+    *reinterpret_cast<uint4*>(q + 2 * ln.chunk) = make_uint4(r.a.x, r.a.y, r.b.x, r.b.y);
+  } else {
+    q[ln.oa >> 2] = r.a;
+    q[ln.ob >> 2] = r.b;
+  }
 }
 
-// Units (of kRows heads) of rows a warp takes of a kind: it takes every a.splits-th unit of
-// the token's queries, keys and values counted through; first unit for this kind, with
-// `before` units in the kinds before it.
-__device__ __forceinline__ int first_unit(int split, int before, int splits) {
-  const int m = (split - before) % splits;
-  return m < 0 ? m + splits : m;
+// The gains of queries and keys in shared memory, each lane's e and f values side by side.
+template <int D, typename Lane>
+__device__ __forceinline__ void stage_gains(const RopeArgs& a, const Lane& ln,
+                                            float4 (*gains)[D / 8][2]) {
+  if (threadIdx.x < 2 * (D / 8)) {
+    const int part = threadIdx.x / (D / 8);
+    // (threads 0 .. D/8-1 of the block are lanes of chunk threadIdx % (D/8))
+    const float* w = a.norm ? a.w[part] : nullptr;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = w != nullptr ? __ldg(w + ln.col_e(i)) : 1.f;
+      v[4 + i] = w != nullptr ? __ldg(w + ln.col_f(i)) : 1.f;
+    }
+    gains[part][ln.chunk][0] = make_float4(v[0], v[1], v[2], v[3]);
+    gains[part][ln.chunk][1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+  __syncthreads();
+}
+template <int D, typename Lane>
+__device__ __forceinline__ Pairs lane_gain(const float4 (*gains)[D / 8][2], int part,
+                                           const Lane& ln) {
+  const float4 e = gains[part][ln.chunk][0], f = gains[part][ln.chunk][1];
+  Pairs w;
+  w.e[0] = make_float2(e.x, e.y);
+  w.e[1] = make_float2(e.z, e.w);
+  w.f[0] = make_float2(f.x, f.y);
+  w.f[1] = make_float2(f.z, f.w);
+  return w;
+}
+
+// The units of one kind that a warp takes of its token: heads first, first + splits * kRows, ...
+struct RopeShare {
+  int head;   // this lane's first head
+  int units;  // steps it takes (some lanes may have no head in the last)
+};
+template <typename Lane>
+__device__ __forceinline__ RopeShare rope_share(int heads, int split, int splits, const Lane& ln) {
+  const int all = (heads + Lane::kRows - 1) / Lane::kRows;
+  return RopeShare{split * Lane::kRows + ln.sub, all > split ? (all - split + splits - 1) / splits : 0};
 }
 
 // ------------------------------------------------------------------------------ forward
 template <int D, bool kInter>
-__global__ void __launch_bounds__(kRopeThreads) fa_rope_fwd_kernel(const RopeArgs a) {
-  using L = RopeLane<D>;
-  constexpr int U = 4;  // rows per lane in flight
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) fa_rope_fwd_kernel(const RopeArgs a) {
+  using L = RopeLane<D, kInter>;
+  constexpr int U = 4;  // units of a batch
   __shared__ __align__(16) float2 cs_all[kRopeWarps][D / 2];
-  const int warp = threadIdx.x >> 5;
-  const L ln(a, kInter);
+  __shared__ float4 gains[2][D / 8][2];
+  float2* const cs = cs_all[threadIdx.x >> 5];
+  const L ln(a);
+  stage_gains<D>(a, ln, gains);
   const RopeTurns<D> turns(a);
-  const bool packed = a.cu != nullptr;
   const long long items = (long long)a.tokens * a.splits;
-  for (long long it = (long long)blockIdx.x * kRopeWarps + warp; it < items;
-       it += (long long)gridDim.x * kRopeWarps) {
-    const int t = (int)(it / a.splits);
-    const int split = (int)(it - (long long)t * a.splits);
+  const int stride = a.splits * L::kRows;
+  for (long long item = (long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5); item < items;
+       item += (long long)gridDim.x * kRopeWarps) {
+    const int t = a.splits == 1 ? (int)item : (int)(item / a.splits);
+    const int split = (int)(item - (long long)t * a.splits);
     const RopeToken k = rope_token(a, t);
     if (!k.owned) continue;
-    float c[8], s[8];
-    if (k.live) turns.compute(a, k, t, ln, cs_all[warp], c, s);
-    int before = 0;
+    RopeRaw now[U], then[U];
+    auto load = [&](int part, int u, RopeRaw (&raw)[U]) {
+      const RopeShare sh = rope_share(a.x[part].heads, split, a.splits, ln);
+      const RowWalk w = walk_rows(a.x[part], k, sh.head, stride);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        raw[i].a = raw[i].b = make_uint2(0, 0);
+        if (k.live && sh.head + (u + i) * stride < a.x[part].heads)
+          raw[i] = load_row<kInter>(w.at(u + i), ln);
+      }
+    };
+    load(0, 0, now);
+    float2 c[2], s[2];
+    if (k.live) turns.compute(a, k, t, ln, cs, c, s);
 #pragma unroll
     for (int part = 0; part < 3; ++part) {
-      const int heads = a.x[part].heads;
-      const int units = (heads + L::kRows - 1) / L::kRows;
-      const __nv_bfloat16* x = token_rows(a.x[part], k, packed);
-      __nv_bfloat16* y = token_rows(a.y[part], k, packed);
-      Pairs w;
-      int u = first_unit(split, before, a.splits);
-      if (part < 2 && a.norm && u < units) load_gain<kInter>(a.w[part], ln.oa, ln.ob, w);
-      for (; u < units; u += U * a.splits) {
-        uint4 va[U], vb[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int h = (u + i * a.splits) * L::kRows + ln.sub;
-          va[i] = vb[i] = make_uint4(0, 0, 0, 0);
-          if (h < heads && k.live) {
-            va[i] = ld_vec(x + h * a.x[part].sh + ln.oa);
-            vb[i] = ld_vec(x + h * a.x[part].sh + ln.ob);
-          }
+      const int heads = a.y[part].heads;
+      const RopeShare sh = rope_share(heads, split, a.splits, ln);
+      if (sh.units == 0 && part < 2) load(part + 1, 0, now);
+      const RowWalk wy = walk_rows(a.y[part], k, sh.head, stride);
+      for (int u = 0; u < sh.units; u += U) {
+        if (u + U < sh.units) {
+          load(part, u + U, then);
+        } else if (part < 2) {
+          load(part + 1, 0, then);
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-          if (u + i * a.splits >= units) break;
-          const int h = (u + i * a.splits) * L::kRows + ln.sub;
+          if (u + i >= sh.units) break;
+          RopeRaw r = now[i];
           if (part < 2 && k.live) {
-            Pairs p;
-            unpack_pairs<kInter>(va[i], vb[i], p);
+            Pairs p = unpack_pairs<kInter>(r);
             if (a.norm) {
-              float ss = 0.f;
+              float2 ss = __fmul2_rn(p.e[0], p.e[0]);
+              ss = __ffma2_rn(p.e[1], p.e[1], ss);
+              ss = __ffma2_rn(p.f[0], p.f[0], ss);
+              ss = __ffma2_rn(p.f[1], p.f[1], ss);
+              const float2 rs = both(rsqrtf(row_sum<D>(ss.x + ss.y) * (1.f / D) + a.eps));
+              const Pairs w = lane_gain<D>(gains, part, ln);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) ss = fmaf(p.e[j], p.e[j], fmaf(p.f[j], p.f[j], ss));
-              const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + a.eps);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                p.e[j] = p.e[j] * r * w.e[j];
-                p.f[j] = p.f[j] * r * w.f[j];
+              for (int j = 0; j < 2; ++j) {
+                p.e[j] = __fmul2_rn(__fmul2_rn(p.e[j], rs), w.e[j]);
+                p.f[j] = __fmul2_rn(__fmul2_rn(p.f[j], rs), w.f[j]);
               }
             }
             if (ln.turns) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float e = p.e[j], f = p.f[j];
-                p.e[j] = fmaf(e, c[j], -f * s[j]);
-                p.f[j] = fmaf(f, c[j], e * s[j]);
+              for (int j = 0; j < 2; ++j) {
+                const float2 e = p.e[j], f = p.f[j];
+                p.e[j] = make_float2(fmaf(e.x, c[j].x, -f.x * s[j].x),
+                                     fmaf(e.y, c[j].y, -f.y * s[j].y));
+                p.f[j] = __ffma2_rn(e, s[j], __fmul2_rn(f, c[j]));
               }
             }
-            pack_pairs<kInter>(p, va[i], vb[i]);
+            r = pack_pairs<kInter>(p);
           }
-          if (h < heads) {
-            st_vec(y + h * a.y[part].sh + ln.oa, va[i]);
-            st_vec(y + h * a.y[part].sh + ln.ob, vb[i]);
-          }
+          if (sh.head + (u + i) * stride < heads) store_row<kInter>(wy.at(u + i), ln, r);
         }
+#pragma unroll
+        for (int i = 0; i < U; ++i) now[i] = then[i];
       }
-      before += units;
     }
   }
 }
 
 // ------------------------------------------------------------------------------ backward
-// Gains' gradients: every lane adds up its sixteen columns over all rows it meets, a block
+// Gains' gradients: every lane adds up its eight columns over all rows it meets, a block
 // adds its lanes in a fixed order and writes (2, D) sums to a.partial, and
 // fa_rope_reduce_kernel adds the blocks: no atomics, so the result is the same on every run.
 template <int D, bool kInter>
-__global__ void __launch_bounds__(kRopeThreads, 2) fa_rope_bwd_kernel(const RopeArgs a) {
-  using L = RopeLane<D>;
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) fa_rope_bwd_kernel(const RopeArgs a) {
+  using L = RopeLane<D, kInter>;
   constexpr int U = 2;
   __shared__ __align__(16) float2 cs_all[kRopeWarps][D / 2];
+  __shared__ float4 gains[2][D / 8][2];
   __shared__ float sums[kRopeWarps][2][D];
   const int warp = threadIdx.x >> 5;
-  const L ln(a, kInter);
+  float2* const cs = cs_all[warp];
+  const L ln(a);
+  stage_gains<D>(a, ln, gains);
   const RopeTurns<D> turns(a);
-  const bool packed = a.cu != nullptr;
   const long long items = (long long)a.tokens * a.splits;
+  const int stride = a.splits * L::kRows;
   Pairs acc[2];
 #pragma unroll
   for (int part = 0; part < 2; ++part)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[part < 2 ? part : 0].e[j] = acc[part < 2 ? part : 0].f[j] = 0.f;
-  for (long long it = (long long)blockIdx.x * kRopeWarps + warp; it < items;
-       it += (long long)gridDim.x * kRopeWarps) {
-    const int t = (int)(it / a.splits);
-    const int split = (int)(it - (long long)t * a.splits);
+    for (int j = 0; j < 2; ++j) acc[part].e[j] = acc[part].f[j] = both(0.f);
+  for (long long item = (long long)blockIdx.x * kRopeWarps + warp; item < items;
+       item += (long long)gridDim.x * kRopeWarps) {
+    const int t = a.splits == 1 ? (int)item : (int)(item / a.splits);
+    const int split = (int)(item - (long long)t * a.splits);
     const RopeToken k = rope_token(a, t);
     if (!k.owned) continue;
-    float c[8], s[8];
-    if (k.live) turns.compute(a, k, t, ln, cs_all[warp], c, s);
-    int before = 0;
+    RopeRaw dy0[U], dy1[U], x0[U], x1[U];
+    auto load = [&](int part, int u, RopeRaw (&dy)[U], RopeRaw (&x)[U]) {
+      const RopeShare sh = rope_share(a.y[part].heads, split, a.splits, ln);
+      const RowWalk wy = walk_rows(a.y[part], k, sh.head, stride);
+      const RowWalk wx = walk_rows(a.x[part], k, sh.head, stride);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        dy[i].a = dy[i].b = x[i].a = x[i].b = make_uint2(0, 0);
+        if (k.live && sh.head + (u + i) * stride < a.y[part].heads) {
+          dy[i] = load_row<kInter>(wy.at(u + i), ln);
+          if (part < 2 && a.norm) x[i] = load_row<kInter>(wx.at(u + i), ln);
+        }
+      }
+    };
+    load(0, 0, dy0, x0);
+    float2 c[2], s[2];
+    if (k.live) turns.compute(a, k, t, ln, cs, c, s);
 #pragma unroll
     for (int part = 0; part < 3; ++part) {
-      const int heads = a.y[part].heads;
-      const int units = (heads + L::kRows - 1) / L::kRows;
-      const bool normed = part < 2 && a.norm;
-      const __nv_bfloat16* x = normed ? token_rows(a.x[part], k, packed) : nullptr;
-      const __nv_bfloat16* y = token_rows(a.y[part], k, packed);
-      __nv_bfloat16* g = token_rows(a.g[part], k, packed);
-      Pairs w;
-      int u = first_unit(split, before, a.splits);
-      if (normed && u < units) load_gain<kInter>(a.w[part], ln.oa, ln.ob, w);
-      for (; u < units; u += U * a.splits) {
-        uint4 ya[U], yb[U], xa[U], xb[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int h = (u + i * a.splits) * L::kRows + ln.sub;
-          ya[i] = yb[i] = xa[i] = xb[i] = make_uint4(0, 0, 0, 0);
-          if (h < heads && k.live) {
-            ya[i] = ld_vec(y + h * a.y[part].sh + ln.oa);
-            yb[i] = ld_vec(y + h * a.y[part].sh + ln.ob);
-            if (normed) {
-              xa[i] = ld_vec(x + h * a.x[part].sh + ln.oa);
-              xb[i] = ld_vec(x + h * a.x[part].sh + ln.ob);
-            }
-          }
+      const int heads = a.g[part].heads;
+      const RopeShare sh = rope_share(heads, split, a.splits, ln);
+      if (sh.units == 0 && part < 2) load(part + 1, 0, dy0, x0);
+      const RowWalk wg = walk_rows(a.g[part], k, sh.head, stride);
+      for (int u = 0; u < sh.units; u += U) {
+        if (u + U < sh.units) {
+          load(part, u + U, dy1, x1);
+        } else if (part < 2) {
+          load(part + 1, 0, dy1, x1);
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-          if (u + i * a.splits >= units) break;
-          const int h = (u + i * a.splits) * L::kRows + ln.sub;
+          if (u + i >= sh.units) break;
+          RopeRaw r = dy0[i];
           if (part < 2 && k.live) {
-            Pairs d;
-            unpack_pairs<kInter>(ya[i], yb[i], d);
+            Pairs d = unpack_pairs<kInter>(r);
             if (ln.turns) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float e = d.e[j], f = d.f[j];
-                d.e[j] = fmaf(e, c[j], f * s[j]);
-                d.f[j] = fmaf(f, c[j], -e * s[j]);
+              for (int j = 0; j < 2; ++j) {
+                const float2 e = d.e[j], f = d.f[j];
+                d.e[j] = __ffma2_rn(f, s[j], __fmul2_rn(e, c[j]));
+                d.f[j] = make_float2(fmaf(f.x, c[j].x, -e.x * s[j].x),
+                                     fmaf(f.y, c[j].y, -e.y * s[j].y));
               }
             }
             if (a.norm) {
-              Pairs p;
-              unpack_pairs<kInter>(xa[i], xb[i], p);
-              float ss = 0.f, sx = 0.f;
+              const Pairs p = unpack_pairs<kInter>(x0[i]);
+              const Pairs w = lane_gain<D>(gains, part, ln);
+              float2 ss = __fmul2_rn(p.e[0], p.e[0]);
+              ss = __ffma2_rn(p.e[1], p.e[1], ss);
+              ss = __ffma2_rn(p.f[0], p.f[0], ss);
+              ss = __ffma2_rn(p.f[1], p.f[1], ss);
+              Pairs gx;  // g o x: the gain's gradient up to the row's r
+              float2 sx = both(0.f);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                ss = fmaf(p.e[j], p.e[j], fmaf(p.f[j], p.f[j], ss));
-                sx = fmaf(d.e[j] * w.e[j], p.e[j], fmaf(d.f[j] * w.f[j], p.f[j], sx));
+              for (int j = 0; j < 2; ++j) {
+                gx.e[j] = __fmul2_rn(d.e[j], p.e[j]);
+                gx.f[j] = __fmul2_rn(d.f[j], p.f[j]);
+                sx = __ffma2_rn(gx.e[j], w.e[j], __ffma2_rn(gx.f[j], w.f[j], sx));
               }
-              // (lanes of rows past the last head hold zeros: they add nothing)
-              const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + a.eps);
-              const float m = row_sum<D>(sx) * r * r * (1.f / D);  // times x: x^ mean(...)
+              // (rows of no head hold zeros: they add nothing)
+              const float rs = rsqrtf(row_sum<D>(ss.x + ss.y) * (1.f / D) + a.eps);
+              const float2 m = both(row_sum<D>(sx.x + sx.y) * rs * rs * (-1.f / D));
+              const float2 r2 = both(rs);
+              Pairs& sum = acc[part < 2 ? part : 0];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                acc[part < 2 ? part : 0].e[j] = fmaf(d.e[j], p.e[j] * r, acc[part < 2 ? part : 0].e[j]);
-                acc[part < 2 ? part : 0].f[j] = fmaf(d.f[j], p.f[j] * r, acc[part < 2 ? part : 0].f[j]);
-                d.e[j] = r * fmaf(-m, p.e[j], d.e[j] * w.e[j]);
-                d.f[j] = r * fmaf(-m, p.f[j], d.f[j] * w.f[j]);
+              for (int j = 0; j < 2; ++j) {
+                sum.e[j] = __ffma2_rn(gx.e[j], r2, sum.e[j]);
+                sum.f[j] = __ffma2_rn(gx.f[j], r2, sum.f[j]);
+                d.e[j] = __fmul2_rn(__ffma2_rn(p.e[j], m, __fmul2_rn(d.e[j], w.e[j])), r2);
+                d.f[j] = __fmul2_rn(__ffma2_rn(p.f[j], m, __fmul2_rn(d.f[j], w.f[j])), r2);
               }
             }
-            pack_pairs<kInter>(d, ya[i], yb[i]);
+            r = pack_pairs<kInter>(d);
           }
-          if (h < heads) {
-            st_vec(g + h * a.g[part].sh + ln.oa, ya[i]);
-            st_vec(g + h * a.g[part].sh + ln.ob, yb[i]);
-          }
+          if (sh.head + (u + i) * stride < heads) store_row<kInter>(wg.at(u + i), ln, r);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          dy0[i] = dy1[i];
+          x0[i] = x1[i];
         }
       }
-      before += units;
     }
   }
   if (a.partial == nullptr) return;
 #pragma unroll
   for (int part = 0; part < 2; ++part) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float e = acc[part < 2 ? part : 0].e[j], f = acc[part < 2 ? part : 0].f[j];
+    for (int j = 0; j < 4; ++j) {
+      float e = j & 1 ? acc[part].e[j / 2].y : acc[part].e[j / 2].x;
+      float f = j & 1 ? acc[part].f[j / 2].y : acc[part].f[j / 2].x;
 #pragma unroll
       for (int off = L::kLanes; off < 32; off <<= 1) {
         e += __shfl_xor_sync(0xffffffffu, e, off);
         f += __shfl_xor_sync(0xffffffffu, f, off);
       }
       if (ln.sub == 0) {
-        // the columns of unpack_pairs' members
-        const int ce = kInter ? (j < 4 ? ln.oa + 2 * j : ln.ob + 2 * (j - 4)) : ln.oa + j;
-        const int cf = kInter ? ce + 1 : ln.ob + j;
-        sums[warp][part][ce] = e;
-        sums[warp][part][cf] = f;
+        sums[warp][part][ln.col_e(j)] = e;
+        sums[warp][part][ln.col_f(j)] = f;
       }
     }
   }

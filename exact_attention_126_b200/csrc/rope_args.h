@@ -24,7 +24,7 @@ struct RopeArgs {
   float* partial;     // backward: per-block sums, (blocks, 2, D)
   int norm;
   float eps;
-  int rot;                  // rotary_dim: a multiple of 16, at most D; 0 = no rotation
+  int rot;                  // rotary_dim: a multiple of 8, at most D; 0 = no rotation
   int axes;
   const float* inv_freq;    // rot / 2
   const uint8_t* pair_axis; // rot / 2, or null (axis 0)
@@ -39,6 +39,10 @@ struct RopeArgs {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
+// Blocks an SM holds (128 registers per thread); the kernels' grids are persistent. With three or
+// four blocks ptxas spills, which costs more than the further warps give (backward on 32 x 2048
+// tokens of 3 x 16 heads of 64: 234 us with two blocks, 398 with three).
+constexpr int kRopeBlocksPerSm = 2;
 // Blocks of the backward at most: its workspace holds the gains' sums of each.
 constexpr int kRopeMaxBlocks = 512;
 

@@ -419,7 +419,7 @@ fa_status_t fa_bwd_noalloc(const void *q, const void *k, const void *v, const vo
  * and token n is the n-th of the tensor. A null pointer or heads = 0 means none of that kind;
  * both sides of a call have the same heads of each kind (FA_ERR_INVALID_ARG). Heads need not be
  * the same for queries, keys and values. B N heads d (packed: total_tokens heads d) must be
- * below 2^31 (FA_ERR_UNSUPPORTED).
+ * below 2^31, and the rows of one kind lie within 2^34 elements (FA_ERR_UNSUPPORTED).
  */
 typedef struct {
     void *data;
@@ -446,7 +446,7 @@ typedef struct {
  *               behind the last, past N) are neither read nor written. Exclusive with
  *               seq_lengths (FA_ERR_INVALID_ARG).
  *   eps         finite, >= 0.
- *   rotary_dim  a multiple of 16 in [0, d] (else FA_ERR_UNSUPPORTED); 0: no rotation.
+ *   rotary_dim  a multiple of 8 in [0, d] (else FA_ERR_UNSUPPORTED); 0: no rotation.
  *   axes        1 .. FA_MAX_AXES (above: FA_ERR_UNSUPPORTED); not looked at without rotation.
  */
 #define FA_MAX_AXES 3

@@ -52,13 +52,14 @@ def test_forward_refusals(lib):
     assert fwd(lib, qo=rows(batch_stride=64)) == 1
     assert fwd(lib, B=1 << 20, N=1 << 10) == 2          # 2^31 elements and more
     assert fwd(lib, B=1 << 16, N=1 << 15) == 2
+    assert fwd(lib, q=rows(batch_stride=1 << 34)) == 2  # rows further apart than 2^34 elements
     assert lib.fa_qk_norm_rope_fwd(rows(), rows(), None, rows(), rows(), None, 2, 5, 64, None,
                                    None) == 1
 
 
 def test_parameter_refusals(lib):
     assert fwd(lib, p=params(rotary_dim=-16)) == 1
-    assert fwd(lib, p=params(rotary_dim=24)) == 2
+    assert fwd(lib, p=params(rotary_dim=20)) == 2
     assert fwd(lib, p=params(rotary_dim=80)) == 2
     assert fwd(lib, p=params(inv_freq=None)) == 1
     assert fwd(lib, p=params(inv_freq=A + 2)) == 3
