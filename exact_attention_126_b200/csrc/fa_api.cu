@@ -214,18 +214,16 @@ fa_status_t resolve_options(const fa_options_t* opt, Extras* x) {
 }
 
 // The cap and the prefixes of a _score call, checked and added to x. A prefix is for causal
-// problems without a left window. The cap's factors (scale / c, its inverse, c log2 e) have to
-// be ordinary fp32 numbers.
+// problems without a left window. scale / c lies in a range in which the powers of it that the
+// kernels work with (score.cuh) are ordinary fp32 numbers.
 fa_status_t resolve_score(const fa_score_t* score, float scale, int causal, fa_window_t window,
                           Extras* x) {
   if (score == nullptr) return FA_OK;
   const float c = score->softcap;
   if (!std::isfinite(c) || c < 0.f) return FA_ERR_INVALID_ARG;
   if (c > 0.f) {
-    const float u = scale / c;
-    if (!std::isnormal(u) || !std::isfinite(u * 4.f) || !std::isnormal(0.625f / u) ||
-        !std::isnormal(c) || !std::isfinite(c * 2.f))
-      return FA_ERR_INVALID_ARG;
+    const double u = (double)scale / c;
+    if (!(u >= 1e-6 && u <= 1e6) || !(c >= 1e-30f && c <= 1e30f)) return FA_ERR_INVALID_ARG;
   }
   if (score->prefix_lengths != nullptr) {
     if ((reinterpret_cast<uintptr_t>(score->prefix_lengths) & 3u) != 0) return FA_ERR_MISALIGNED;

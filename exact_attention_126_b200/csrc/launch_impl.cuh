@@ -166,12 +166,6 @@ inline fa_status_t launched() {
 }
 
 
-// The cap of the scores as the kFeatScore kernels take it (score.cuh).
-inline fa::CapArgs cap_args(const Extras& x, float scale) {
-  const float u = x.softcap > 0.f ? scale / x.softcap : 1.f;
-  return fa::CapArgs{x.softcap > 0.f ? 1 : 0, u, 0.625f / u, x.softcap * fa::kLog2e};
-}
-
 template <int D, int kFeat>
 fa_status_t launch_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
                        const Problem& pb, const Extras& x, int fault, cudaStream_t st) {
@@ -225,7 +219,7 @@ fa_status_t launch_fwd(const void* q, const void* k, const void* v, void* o, flo
   a.total = x.total;
   a.o_scale = x.o_scale;
   a.prefix = x.prefix;
-  a.cap = cap_args(x, scale);
+  a.cap = fa::make_cap(x.softcap, scale);
   const int grid = persistent_grid(a);
   fa::fa_fwd_kernel<D, kFeat><<<grid, C::kThreads, smem, st>>>(mq, mkk, mv, a);
   return launched();
@@ -282,7 +276,7 @@ inline fa::BwdArgs bwd_args(const void* ws, const Problem& pb, const Extras& x) 
   a.cu = x.cu;
   a.total = x.total;
   a.prefix = x.prefix;
-  a.cap = cap_args(x, scale);
+  a.cap = fa::make_cap(x.softcap, scale);
   return a;
 }
 

@@ -6,10 +6,11 @@
 //
 // tanh costs two special-function operations (tanh u = 1 - 2 / (1 + e^(2u))), three times what the
 // softmax itself needs per score, and that unit is a co-ceiling of the attention kernels. But a cap
-// is chosen so that few scores come near it: for |u| <= 0.625 an odd polynomial of degree 9 (u times
-// a quartic in u^2, my minimax fit of tanh(u) / u on that range, relative error 1.1e-7) takes seven
-// packed fp32 instructions per two scores and keeps the relative accuracy of small scores, which
-// matters for large caps. A warp whose scores all lie there takes it; otherwise the exact form.
+// is chosen so that few scores come near it: for |u| <= 0.4 an odd polynomial of degree 7 (u times a
+// cubic in u^2, my minimax fit of tanh(u) / u on that range, relative error 1e-7) takes five packed
+// fp32 instructions per two scores and keeps the relative accuracy of small scores, which matters
+// for large caps. A warp whose scores all lie there takes it; otherwise the exact form. The powers
+// of 1 / c are multiplied into the coefficients, so that s itself is what the polynomial takes.
 #pragma once
 
 #include "sm100.cuh"
@@ -19,10 +20,29 @@ namespace fa {
 
 struct CapArgs {
   int on;       // 0: the scores are not capped
-  float u;      // scale / c: turns Q K^T into u
-  float limit;  // |Q K^T| up to which the polynomial holds: 0.625 c / scale
+  float limit;  // |Q K^T| up to which the polynomial holds: 0.4 c / scale
   float mul;    // c log2(e): turns tanh(u) into log2 units
+  float exp2u;  // 2 log2(e) scale / c
+  float a[4];   // the polynomial in (Q K^T)^2
 };
+
+// The arguments for a cap c of scores scaled by `scale`; c = 0: none.
+inline CapArgs make_cap(float c, float scale) {
+  CapArgs r = {};
+  if (!(c > 0.f)) return r;
+  const double u = (double)scale / c;
+  r.on = 1;
+  r.limit = (float)(0.4 / u);
+  r.mul = (float)(c * 1.4426950408889634);
+  r.exp2u = (float)(2.0 * 1.4426950408889634 * u);
+  const double fit[4] = {0.999999902, -0.333313625, 0.132709767, -0.047553602};
+  double p = u;
+  for (int i = 0; i < 4; ++i) {
+    r.a[i] = (float)(fit[i] * p);
+    p *= u * u;
+  }
+  return r;
+}
 
 __device__ __forceinline__ float rcp(float x) {
   float y;
@@ -30,7 +50,7 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// x <- tanh(x * cap.u), for the N scores of each lane of a warp.
+// x <- tanh(u) of the N scores x of each lane of a warp.
 template <int N>
 __device__ __forceinline__ void cap_tanh(float (&x)[N], const CapArgs& cap) {
   float m[4] = {0.f, 0.f, 0.f, 0.f};
@@ -38,22 +58,20 @@ __device__ __forceinline__ void cap_tanh(float (&x)[N], const CapArgs& cap) {
   for (int i = 0; i < N; i += 2)
     m[(i >> 1) & 3] = fmax3(m[(i >> 1) & 3], fabsf(x[i]), fabsf(x[i + 1]));
   if (__any_sync(0xffffffffu, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) > cap.limit)) {
-    const float k = 2.f * kLog2e * cap.u;
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = fmaf(-2.f, rcp(ex2(x[i] * k) + 1.f), 1.f);
+    for (int i = 0; i < N; ++i) x[i] = fmaf(-2.f, rcp(ex2(x[i] * cap.exp2u) + 1.f), 1.f);
     return;
   }
-  const float2 ku = make_float2(cap.u, cap.u);
+  const float2 a0 = make_float2(cap.a[0], cap.a[0]), a1 = make_float2(cap.a[1], cap.a[1]);
+  const float2 a2 = make_float2(cap.a[2], cap.a[2]), a3 = make_float2(cap.a[3], cap.a[3]);
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
-    const float2 u = __fmul2_rn(make_float2(x[i], x[i + 1]), ku);
-    const float2 z = __fmul2_rn(u, u);
-    float2 p = __ffma2_rn(z, make_float2(0.0150509423f, 0.0150509423f),
-                          make_float2(-0.0518218645f, -0.0518218645f));
-    p = __ffma2_rn(p, z, make_float2(0.133045259f, 0.133045259f));
-    p = __ffma2_rn(p, z, make_float2(-0.333319542f, -0.333319542f));
-    p = __ffma2_rn(p, z, make_float2(0.999999893f, 0.999999893f));
-    p = __fmul2_rn(p, u);
+    const float2 s = make_float2(x[i], x[i + 1]);
+    const float2 z = __fmul2_rn(s, s);
+    float2 p = __ffma2_rn(z, a3, a2);
+    p = __ffma2_rn(p, z, a1);
+    p = __ffma2_rn(p, z, a0);
+    p = __fmul2_rn(p, s);
     x[i] = p.x;
     x[i + 1] = p.y;
   }

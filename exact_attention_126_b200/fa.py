@@ -8,7 +8,6 @@ library's kernels; if the library cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 
@@ -165,7 +164,8 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # (the raw handle: building a torch.cuda.Stream costs several microseconds per call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -410,6 +410,23 @@ def fa_version() -> int:
 
 
 # ------------------------------------------------------------------ allocating helpers
+def _elsewhere(t):
+    """Whether `t` lives on another CUDA device than the current one (the library launches on
+    the current device)."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    return t.get_device() != torch.cuda.current_device()
+
+
+def _scratch(nbytes, device, stream):
+    """A workspace that stays out of the allocator's hands until `stream` (None: the current
+    one) has passed the kernels launched on it."""
+    ws = torch.empty(max(1, nbytes), dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(torch.cuda.ExternalStream(_stream(stream), device=device))
+    return ws
+
+
 def _check_inputs(*ts):
     for t in ts:
         if not t.is_cuda:
@@ -490,6 +507,11 @@ def attention_forward(q, k, v, scale=None, causal=False, window=(-1, -1), stream
     cu_seqlens[b+1]-1; O is (total, H, d) and LSE (H, total). softcap (c > 0): the scaled scores
     s become c tanh(s / c). prefix_lengths ((B,) int32), for causal problems: query i of
     sequence b also sees every key j < prefix_lengths[b]."""
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return attention_forward(q, k, v, scale, causal, window, stream, alibi_slopes,
+                                     key_padding, keep_residual, dropout, seq_lengths, cu_seqlens,
+                                     max_seqlen, softcap, prefix_lengths)
     _check_inputs(q, k, v)
     if cu_seqlens is not None:
         B, H, N, d = _packed_dims(q, cu_seqlens, max_seqlen, seq_lengths)
@@ -530,6 +552,12 @@ def attention_backward(q, k, v, o, lse, do, scale=None, causal=False, window=(-1
     prefix_lengths.
     fused: at head_dim 64, the backward in one pass over key tiles with dQ added up in fp32
     in no fixed order (see FA_BWD_FUSED); otherwise the deterministic dK/dV and dQ passes."""
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return attention_backward(q, k, v, o, lse, do, scale, causal, window, stream,
+                                      alibi_slopes, key_padding, o_low, dropout, fused,
+                                      seq_lengths, cu_seqlens, max_seqlen, softcap,
+                                      prefix_lengths)
     _check_inputs(q, k, v, o, do)
     if cu_seqlens is not None:
         B, H, N, d = _packed_dims(q, cu_seqlens, max_seqlen, seq_lengths)
@@ -539,10 +567,9 @@ def attention_backward(q, k, v, o, lse, do, scale=None, causal=False, window=(-1
     dq = torch.empty_like(q)
     dk = torch.empty_like(q)
     dv = torch.empty_like(q)
-    ws = torch.empty(max(1, fa_bwd_workspace_bytes_ex(
+    ws = _scratch(fa_bwd_workspace_bytes_ex(
         B, H, N, d, options(fused=fused, seq_lengths=seq_lengths, cu_seqlens=cu_seqlens,
-                            total_tokens=total))),
-                     dtype=torch.uint8, device=q.device)
+                            total_tokens=total)), q.device, stream)
     if alibi_slopes is not None:
         _check_slopes(alibi_slopes, q)
     if key_padding is not None:
@@ -569,66 +596,62 @@ def attention_backward(q, k, v, o, lse, do, scale=None, causal=False, window=(-1
 
 
 # ------------------------------------------------- per-head norm and rotary positions
-def _check_rows(t, name, like, tokens, d):
-    """A bf16 CUDA tensor of (tokens..., heads, d) rows on `like`'s device, d consecutive."""
-    if t.dtype != torch.bfloat16 or t.device != like.device or not t.is_cuda:
+_BF16 = torch.bfloat16
+
+
+def _rows(t, name, tokens, d, device, heads_at):
+    """The fa_heads_t of a bf16 tensor of any strides, token-major (B, N, heads, d), head-major
+    (B, heads, N, d) (heads_at 2, 1) or packed (total, heads, d) (heads_at 1), checked to have
+    the given tokens and head_dim, d consecutive, on `device`; None for None."""
+    if t is None:
+        return None
+    shape, st = t.shape, t.stride()
+    if t.dtype != _BF16 or t.device != device:
         raise ValueError("%s must be a bf16 tensor on the queries' CUDA device" % name)
-    if t.dim() != len(tokens) + 2 or tuple(t.shape[:-2]) != tokens or t.shape[-1] != d:
-        raise ValueError("%s must have the queries' tokens and head_dim" % name)
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError("%s must hold each head's values consecutively" % name)
+    if len(tokens) == 2:
+        if len(shape) != 4 or shape[0] != tokens[0] or shape[3 - heads_at] != tokens[1]:
+            raise ValueError("%s must be a 4-D tensor of the queries' tokens" % name)
+        strides = (st[0], st[3 - heads_at], st[heads_at])
+    else:
+        if len(shape) != 3 or shape[0] != tokens[0]:
+            raise ValueError("%s must be a (total, heads, head_dim) tensor of the queries' tokens"
+                             % name)
+        strides = (0, st[0], st[1])
+    if shape[-1] != d or st[-1] != 1:
+        raise ValueError("%s must hold head_dim consecutive values per head" % name)
+    return fa_heads_t(t.data_ptr(), shape[heads_at], *strides)
 
 
-def _projection_rows(t):
-    """The fa_heads_t of a (B, N, H, d) or packed (total, H, d) tensor of any strides."""
+def _aux(t, name, dtype, device, shape):
+    """The address of a contiguous tensor of the given type and shape on `device` (0: None)."""
     if t is None:
         return None
-    st = t.stride()
-    if len(st) == 4:
-        return fa_heads_t(t.data_ptr(), t.shape[2], st[0], st[1], st[2])
-    return fa_heads_t(t.data_ptr(), t.shape[1], 0, st[0], st[1])
-
-
-def _attention_rows(t):
-    """The fa_heads_t of a (B, H, N, d) or packed (total, H, d) tensor."""
-    if t is None:
-        return None
-    st = t.stride()
-    if len(st) == 4:
-        return fa_heads_t(t.data_ptr(), t.shape[1], st[0], st[2], st[1])
-    return fa_heads_t(t.data_ptr(), t.shape[1], 0, st[0], st[1])
-
-
-def _check_aux(t, name, dtype, like, shape):
-    if t.dtype != dtype or t.device != like.device or not t.is_contiguous():
+    if t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor on the queries' device"
                          % (name, str(dtype).replace("torch.", "")))
-    if tuple(t.shape) != shape:
-        raise ValueError("%s must have shape %s" % (name, shape))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s" % (name, tuple(shape)))
+    return t.data_ptr()
 
 
-def _norm_rope_params(like, tokens, d, q_weight, k_weight, eps, norm, inv_freq, positions,
+def _norm_rope_params(device, tokens, d, q_weight, k_weight, eps, norm, inv_freq, positions,
                       pair_axis, interleaved, seq_lengths, cu_seqlens, max_seqlen):
-    """(B, N, fa_norm_rope_t) of a call on (tokens..., H, d) rows."""
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            if not norm:
-                raise ValueError("%s is a gain of the norm" % name)
-            _check_aux(w, name, torch.float32, like, (d,))
+    """(B, N, fa_norm_rope_t) of a call on rows of `tokens`."""
+    if not norm and (q_weight is not None or k_weight is not None):
+        raise ValueError("q_weight and k_weight are gains of the norm")
     rot, axes = 0, 1
+    freq = pos = axis = lens = cu = None
     if inv_freq is not None:
-        if inv_freq.dim() != 1:
-            raise ValueError("inv_freq must hold one frequency per rotation")
-        _check_aux(inv_freq, "inv_freq", torch.float32, like, (inv_freq.numel(),))
-        rot = 2 * inv_freq.numel()
+        half = inv_freq.numel()
+        rot = 2 * half
+        freq = _aux(inv_freq, "inv_freq", torch.float32, device, (half,))
         if positions is not None:
             if positions.dim() == len(tokens) + 1:
                 axes = positions.shape[0]
-                _check_aux(positions, "positions", torch.int32, like, (axes,) + tokens)
+                pos = _aux(positions, "positions", torch.int32, device, (axes,) + tokens)
             else:
-                _check_aux(positions, "positions", torch.int32, like, tokens)
-        if pair_axis is not None:
-            _check_aux(pair_axis, "pair_axis", torch.uint8, like, (rot // 2,))
+                pos = _aux(positions, "positions", torch.int32, device, tokens)
+        axis = _aux(pair_axis, "pair_axis", torch.uint8, device, (half,))
     elif positions is not None or pair_axis is not None:
         raise ValueError("positions and pair_axis need inv_freq")
     total = 0
@@ -637,44 +660,24 @@ def _norm_rope_params(like, tokens, d, q_weight, k_weight, eps, norm, inv_freq, 
             raise ValueError("seq_lengths and cu_seqlens exclude each other")
         if len(tokens) != 1:
             raise ValueError("a packed batch takes (total_tokens, heads, head_dim) tensors")
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        B = cu_seqlens.numel() - 1
+        cu = _aux(cu_seqlens, "cu_seqlens", torch.int32, device, (B + 1,))
+        if B < 1:
             raise ValueError("cu_seqlens must hold B + 1 >= 2 offsets")
-        _check_aux(cu_seqlens, "cu_seqlens", torch.int32, like, (cu_seqlens.numel(),))
         if max_seqlen is None or int(max_seqlen) < 1:
             raise ValueError("a packed batch needs max_seqlen >= 1 (the longest sequence)")
-        B, N, total = cu_seqlens.numel() - 1, int(max_seqlen), tokens[0]
+        N, total = int(max_seqlen), tokens[0]
     else:
         if len(tokens) != 2:
             raise ValueError("(total_tokens, heads, head_dim) tensors need cu_seqlens")
         B, N = tokens
-        if seq_lengths is not None:
-            _check_aux(seq_lengths, "seq_lengths", torch.int32, like, (B,))
-    return B, N, fa_norm_rope_t(_ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(pair_axis),
-                                _ptr(positions), _ptr(seq_lengths), _ptr(cu_seqlens), eps,
-                                1 if norm else 0, rot, axes, 1 if interleaved else 0, total)
+        lens = _aux(seq_lengths, "seq_lengths", torch.int32, device, (B,))
+    return B, N, fa_norm_rope_t(_aux(q_weight, "q_weight", torch.float32, device, (d,)),
+                                _aux(k_weight, "k_weight", torch.float32, device, (d,)),
+                                freq, axis, pos, lens, cu, eps, 1 if norm else 0, rot, axes,
+                                1 if interleaved else 0, total)
 
 
-def _on_device(fn):
-    """Runs a call on the device its first tensor is on, whichever device is current."""
-    @functools.wraps(fn)
-    def call(t, *args, **kw):
-        if t.is_cuda and t.device.index != torch.cuda.current_device():
-            with torch.cuda.device(t.device):
-                return fn(t, *args, **kw)
-        return fn(t, *args, **kw)
-    return call
-
-
-def _scratch(nbytes, device, stream):
-    """A workspace that stays out of the allocator's hands until `stream` (None: the current
-    one) has passed the kernels launched on it."""
-    ws = torch.empty(max(1, nbytes), dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(torch.cuda.ExternalStream(_stream(stream), device=device))
-    return ws
-
-
-@_on_device
 def qk_norm_rope_forward(q, k, v=None, q_weight=None, k_weight=None, eps=1e-6, norm=True,
                          inv_freq=None, positions=None, pair_axis=None, interleaved=False,
                          seq_lengths=None, cu_seqlens=None, max_seqlen=None, stream=None):
@@ -689,29 +692,35 @@ def qk_norm_rope_forward(q, k, v=None, q_weight=None, k_weight=None, eps=1e-6, n
     no rotation. positions ((B, N) or (total,) int32; None = the place in the sequence): with
     several axes (axes, B, N) or (axes, total), and pair_axis (rotary_dim / 2 uint8) names each
     rotation's axis. seq_lengths ((B,) int32): rows past a length are zero."""
-    tokens, d = tuple(q.shape[:-2]), q.shape[-1]
-    _check_rows(q, "q", q, tokens, d)
-    _check_rows(k, "k", q, tokens, d)
-    if v is not None:
-        _check_rows(v, "v", q, tokens, d)
-    B, N, params = _norm_rope_params(q, tokens, d, q_weight, k_weight, eps, norm, inv_freq,
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return qk_norm_rope_forward(q, k, v, q_weight, k_weight, eps, norm, inv_freq,
+                                        positions, pair_axis, interleaved, seq_lengths,
+                                        cu_seqlens, max_seqlen, stream)
+    tokens, d, device = tuple(q.shape[:-2]), q.shape[-1], q.device
+    at = len(tokens)
+    ins = (_rows(q, "q", tokens, d, device, at), _rows(k, "k", tokens, d, device, at),
+           _rows(v, "v", tokens, d, device, at))
+    B, N, params = _norm_rope_params(device, tokens, d, q_weight, k_weight, eps, norm, inv_freq,
                                      positions, pair_axis, interleaved, seq_lengths, cu_seqlens,
                                      max_seqlen)
-    outs = []
-    for t in (q, k, v):
-        if t is None:
+    res, outs = [], []
+    for r in ins:
+        if r is None:
             outs.append(None)
-        elif len(tokens) == 2:
-            outs.append(torch.empty((B, t.shape[2], N, d), dtype=t.dtype, device=t.device))
+            continue
+        h = r.heads
+        if at == 2:
+            t = q.new_empty((B, h, N, d))
+            outs.append(fa_heads_t(t.data_ptr(), h, h * N * d, d, N * d))
         else:
-            outs.append(torch.empty((tokens[0], t.shape[1], d), dtype=t.dtype, device=t.device))
-    fa_qk_norm_rope_fwd(_projection_rows(q), _projection_rows(k), _projection_rows(v),
-                        _attention_rows(outs[0]), _attention_rows(outs[1]),
-                        _attention_rows(outs[2]), B, N, d, params, stream)
-    return tuple(outs) if v is not None else tuple(outs[:2])
+            t = q.new_empty((tokens[0], h, d))
+            outs.append(fa_heads_t(t.data_ptr(), h, 0, h * d, d))
+        res.append(t)
+    fa_qk_norm_rope_fwd(*ins, *outs, B, N, d, params, stream)
+    return tuple(res)
 
 
-@_on_device
 def qk_norm_rope_backward(dq, dk, dv=None, q=None, k=None, q_weight=None, k_weight=None, eps=1e-6,
                           norm=True, inv_freq=None, positions=None, pair_axis=None,
                           interleaved=False, seq_lengths=None, cu_seqlens=None, max_seqlen=None,
@@ -722,48 +731,42 @@ def qk_norm_rope_backward(dq, dk, dv=None, q=None, k=None, q_weight=None, k_weig
     (needed with norm). out: three tensors (the third None without dv) of the forward's input
     shapes, of any strides that do not overlap, to write gq, gk, gv to; by default they are views
     of one new (B, N, heads of all, d) or (total, heads of all, d) tensor."""
-    if dq.dim() not in (3, 4):
+    if _elsewhere(dq):
+        with torch.cuda.device(dq.device):
+            return qk_norm_rope_backward(dq, dk, dv, q, k, q_weight, k_weight, eps, norm,
+                                         inv_freq, positions, pair_axis, interleaved, seq_lengths,
+                                         cu_seqlens, max_seqlen, stream, out)
+    if dq.dim() == 4:
+        tokens = (dq.shape[0], dq.shape[2])
+    elif dq.dim() == 3:
+        tokens = (dq.shape[0],)
+    else:
         raise ValueError("dq must be (B, heads, N, d) or packed (total, heads, d)")
-    packed = dq.dim() == 3
-    # token-major views
-    dqt, dkt, dvt = (t if t is None or packed or t.dim() != 4 else t.transpose(1, 2)
-                     for t in (dq, dk, dv))
-    tokens, d = tuple(dqt.shape[:-2]), dqt.shape[-1]
-    grads = (("dq", dqt), ("dk", dkt)) + ((("dv", dvt),) if dv is not None else ())
-    for name, t in grads:
-        _check_rows(t, name, dq, tokens, d)
-    if norm:
-        if q is None or k is None:
-            raise ValueError("the norm's gradient needs q and k")
-        for name, t, g in (("q", q, dqt), ("k", k, dkt)):
-            _check_rows(t, name, dq, tokens, d)
-            if t.shape != g.shape:
-                raise ValueError("%s must have its gradient's heads" % name)
-    B, N, params = _norm_rope_params(dq, tokens, d, q_weight, k_weight, eps, norm, inv_freq,
+    d, device, at = dq.shape[-1], dq.device, len(tokens)
+    grads = [_rows(t, n, tokens, d, device, 1) for t, n in ((dq, "dq"), (dk, "dk"), (dv, "dv"))]
+    if norm and (q is None or k is None):
+        raise ValueError("the norm's gradient needs q and k")
+    xq = _rows(q, "q", tokens, d, device, at) if norm else None
+    xk = _rows(k, "k", tokens, d, device, at) if norm else None
+    B, N, params = _norm_rope_params(device, tokens, d, q_weight, k_weight, eps, norm, inv_freq,
                                      positions, pair_axis, interleaved, seq_lengths, cu_seqlens,
                                      max_seqlen)
+    heads = [0 if r is None else r.heads for r in grads]
+    if norm and (xq.heads != heads[0] or xk.heads != heads[1]):
+        raise ValueError("q and k must have their gradients' heads")
     if out is None:
-        heads = [t.shape[-2] for _, t in grads]
-        out = list(torch.empty(tokens + (sum(heads), d), dtype=dq.dtype, device=dq.device)
-                   .split(heads, -2))
+        out = list(dq.new_empty(tokens + (sum(heads), d)).split(heads, -2))
     else:
-        out = [t for t in out if t is not None]
-        if len(out) != len(grads):
-            raise ValueError("out must hold one tensor per gradient")
-        for t, (name, g) in zip(out, grads):
-            _check_rows(t, "out", dq, tokens, d)
-            if t.shape != g.shape:
-                raise ValueError("out must have the shapes of the forward's inputs")
+        out = list(out) + [None] * (3 - len(out))
     if dv is None:
-        out.append(None)
+        out[2] = None
+    outs = [_rows(t, "out", tokens, d, device, at) for t in out]
+    if [0 if r is None else r.heads for r in outs] != heads:
+        raise ValueError("out must hold tensors of the forward's input shapes")
     gqw = torch.empty_like(q_weight) if q_weight is not None else None
     gkw = torch.empty_like(k_weight) if k_weight is not None else None
     ws = None
     if gqw is not None or gkw is not None:
-        ws = _scratch(fa_qk_norm_rope_workspace_bytes(d), dq.device, stream)
-    fa_qk_norm_rope_bwd(_projection_rows(dqt), _projection_rows(dkt), _projection_rows(dvt),
-                        _projection_rows(q) if norm else None,
-                        _projection_rows(k) if norm else None,
-                        _projection_rows(out[0]), _projection_rows(out[1]),
-                        _projection_rows(out[2]), gqw, gkw, B, N, d, params, ws, stream)
+        ws = _scratch(fa_qk_norm_rope_workspace_bytes(d), device, stream)
+    fa_qk_norm_rope_bwd(*grads, xq, xk, *outs, gqw, gkw, B, N, d, params, ws, stream)
     return out[0], out[1], out[2], gqw, gkw

@@ -215,8 +215,8 @@ fa_status_t fa_fwd_fp8(const void *q, const void *k, const void *v, float q_scal
  *            [0, real length]. For causal problems (else FA_ERR_INVALID_ARG) without a left
  *            window (else FA_ERR_UNSUPPORTED).
  *   softcap  c > 0 caps the scaled scores s: they become c tanh(s / c), before an ALiBi bias, the
- *            mask and the softmax (LSE is that of the capped scores); 0 = no cap. Finite, >= 0,
- *            and c, scale / c and its inverse ordinary fp32 numbers (else FA_ERR_INVALID_ARG).
+ *            mask and the softmax (LSE is that of the capped scores); 0 = no cap. c in
+ *            [1e-30, 1e30] and scale / c in [1e-6, 1e6] (else FA_ERR_INVALID_ARG).
  */
 typedef struct {
     const int *prefix_lengths;

@@ -281,9 +281,10 @@ def test_in_place():
     q, k, v = x.split((4, 2, 2), 1)
     ref = fa.qk_norm_rope_forward(q, k, v, **kw, **call)
     y = x.clone()
-    B, N, params = fa._norm_rope_params(y, (77,), 128, kw["q_weight"], kw["k_weight"], 1e-6, True,
-                                        kw["inv_freq"], None, None, False, None, cu, 64)
-    parts = [fa._projection_rows(t) for t in y.split((4, 2, 2), 1)]
+    B, N, params = fa._norm_rope_params(y.device, (77,), 128, kw["q_weight"], kw["k_weight"],
+                                        1e-6, True, kw["inv_freq"], None, None, False, None, cu,
+                                        64)
+    parts = [fa._rows(t, "x", (77,), 128, y.device, 1) for t in y.split((4, 2, 2), 1)]
     fa.fa_qk_norm_rope_fwd(*parts, *parts, B, N, 128, params)
     for a, b in zip(y.split((4, 2, 2), 1), ref):
         assert torch.equal(a, b)

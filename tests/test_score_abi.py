@@ -40,8 +40,8 @@ def test_refusals(lib):
         assert f(S(softcap=5.0), fa.fa_options_t(dropout_p=1.0)) == 1
         assert f(S(softcap=5.0), fa.fa_options_t(flags=1)) == 2
         assert f(S(prefix_lengths=A), fa.fa_options_t(flags=1)) == 2
-    assert fwd(S(softcap=1e30), scale=1e-30) == 1   # scale / c is no fp32 number
-    assert fwd(S(softcap=1e-30), scale=1e30) == 1
+    assert fwd(S(softcap=1e6), scale=0.1) == 1      # scale / c outside [1e-6, 1e6]
+    assert fwd(S(softcap=1e-8), scale=0.1) == 1
     assert fwd(S(prefix_lengths=A), window=(5, 0)) == 2
     assert fwd(S(softcap=5.0), q=None) == 1
     assert fwd(S(softcap=5.0), q=A + 8) == 3
