@@ -597,8 +597,9 @@ __global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 
     // what turns a score (kFeatScore with a cap: its tanh) into log2 units
     const float sl2 = kScore && a.cap.on ? a.cap.mul : a.scale_log2;
     int ns = 0;  // S tiles of this stream consumed (all items)
-    int nsh[2] = {0, 0};   // kHalves: S halves consumed, per half
-    int npub[2] = {0, 0};  // kHalves: P halves published, per half
+    // kHalves: key tiles done (each consumed S and published P of either half). One counter in
+    // place of two per half: C5 causal at N 4096, forward 367 -> 350 us
+    int nt = 0;
     bool ok = true;
 
 
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 
                           (keep_bits16(a.drop, blk + 1, (uint32_t)row, (uint32_t)it.bh) << 16);
               }
             }
-            if (!mbar_wait_warp(bar((h ? C::bSFull2 : C::bSFull) + s), nsh[h] & 1, abort_flag)) {
+            if (!mbar_wait_warp(bar((h ? C::bSFull2 : C::bSFull) + s), nt & 1, abort_flag)) {
               ok = false;
               break;
             }
@@ -644,7 +645,7 @@ __global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 
 #pragma unroll
               for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(u[c]);
             }
-            if (kScore && a.cap.on) cap_tanh(x, a.cap);
+            if (kScore && a.cap.on) cap_tanh_tmem(x, a.cap, tSh);
             if (kAlibi) {
               // key minus query index at column 0 of the half
               const long long kq = (long long)j * kBlock + 64 * h - row;
@@ -739,7 +740,7 @@ __global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 
             // half's P V (the last product into O) has completed
             if (!(j == rg.lo && h == 0) && __any_sync(0xffffffffu, grow)) {
               const int hp = h ^ 1;
-              if (!mbar_wait_warp(bar((hp ? C::bODone2 : C::bODone) + s), (npub[hp] - 1) & 1,
+              if (!mbar_wait_warp(bar((hp ? C::bODone2 : C::bODone) + s), (h ? nt : nt - 1) & 1,
                                   abort_flag)) {
                 ok = false;
                 break;
@@ -760,10 +761,9 @@ __global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive_warp(bar((h ? C::bPFull2 : C::bPFull) + s));
-            ++nsh[h];
-            ++npub[h];
           }
           if (!ok) break;
+          ++nt;
           continue;
         }
         // keep flags of this row's 128 weights (they depend on no score, so they are drawn
@@ -782,6 +782,59 @@ __global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 
           break;
         }
         tc_fence_after();
+        float mx = -INFINITY;
+        if constexpr (kScore) {
+          // Everything that changes the scores, and their maximum, in a loop over 32 columns that
+          // takes S from tensor memory and puts it back: with the 128 columns unrolled, as the
+          // kernels without kFeatScore have them, the loop body outgrew the instruction cache
+          // (the top stall; B32 H16 N2048 causal with a cap: 958 us unrolled, 855 us as a loop)
+          const bool whole = tile_all_visible(rg.m, j, mk);
+          int c_lo = 0, c_hi = kBlock - 1;
+          if (!whole) visible_keys(row, (long long)j * kBlock, kBlock, mk, c_lo, c_hi);
+#pragma unroll 1
+          for (int q = 0; q < kBlock / 32; ++q) {
+            uint32_t u[32];
+            tmem_ld32(tS + 32 * q, u);
+            tmem_wait_ld();
+            reg_fence(u);
+            float y[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) y[c] = __uint_as_float(u[c]);
+            if (a.cap.on) cap_tanh(y, a.cap);
+            if (kAlibi) {
+              const float base = (float)((long long)j * kBlock + 32 * q - row);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                y[c] = fmaf(y[c], sl2, -slope2 * fabsf(base + (float)c));
+            }
+            if (!whole) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                y[c] = (c >= c_lo - 32 * q && c <= c_hi - 32 * q) ? y[c] : -INFINITY;
+            }
+            if (kKpad) {
+              const int col = j * kBlock + 32 * q + lane;
+              const uint32_t pm = __ballot_sync(
+                  0xffffffffu, col < a.N && a.kpad[(size_t)(it.bh / a.H) * a.N + col] != 0);
+              if (pm != 0u) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) y[c] = ((pm >> c) & 1u) ? -INFINITY : y[c];
+              }
+            }
+            float t[4] = {y[0], y[1], y[2], y[3]};
+#pragma unroll
+            for (int c = 4; c < 28; c += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) t[e] = fmax3(t[e], y[c + e], y[c + 4 + e]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[e] = fmaxf(t[e], y[28 + e]);
+            mx = fmaxf(mx, fmaxf(fmax3(t[0], t[1], t[2]), t[3]));
+#pragma unroll
+            for (int c = 0; c < 32; ++c) u[c] = __float_as_uint(y[c]);
+            tmem_st32(tS + 32 * q, u);
+          }
+          tmem_wait_st();
+        }
         float x[kBlock];
         {
           // all four loads in flight before one wait
@@ -799,8 +852,7 @@ __global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 
           tc_fence_before();
           mbar_arrive_warp(bar(C::bSFree + s));
         }
-        if (kScore && a.cap.on) cap_tanh(x, a.cap);
-        if (kAlibi) {
+        if (kAlibi && !kScore) {
           // key minus query index at column 0 of the tile
           const long long kq = (long long)j * kBlock - row;
           const float base = (float)kq;
@@ -819,13 +871,13 @@ __global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 
               x[c] = fmaf(x[c], sl2, -slope2 * fabsf(base + (float)c));
           }
         }
-        if (!tile_all_visible(rg.m, j, mk)) {
+        if (!kScore && !tile_all_visible(rg.m, j, mk)) {
           int c_lo, c_hi;
           visible_keys(row, (long long)j * kBlock, kBlock, mk, c_lo, c_hi);
 #pragma unroll
           for (int c = 0; c < kBlock; ++c) x[c] = (c >= c_lo && c <= c_hi) ? x[c] : -INFINITY;
         }
-        if (kKpad) {
+        if (kKpad && !kScore) {
           // padded keys of this tile: lane l reads the flag of key 32g + l, one ballot per
           // 32 keys; the same 128 bits for every row
           uint32_t pm[4];
@@ -841,8 +893,7 @@ __global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 
               x[c] = ((pm[c >> 5] >> (c & 31)) & 1u) ? -INFINITY : x[c];
           }
         }
-        float mx;
-        {
+        if constexpr (!kScore) {
           // 16 partial maxima: x[0..47], then two columns at a time up to x[111], then x[112..127]
           float t[16];
 #pragma unroll
@@ -932,7 +983,7 @@ __global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 
       }
       if (!ok) break;
       // epilogue of the item: O / l and LSE, once the last P V product has completed
-      if (!(C::kHalves ? mbar_wait_warp(bar(C::bODone2 + s), (npub[1] - 1) & 1, abort_flag)
+      if (!(C::kHalves ? mbar_wait_warp(bar(C::bODone2 + s), (nt - 1) & 1, abort_flag)
                        : mbar_wait_warp(bar(C::bODone + s), (ns - 1) & 1, abort_flag))) {
         ok = false;
         break;

@@ -2,9 +2,10 @@
 
 Tolerances: those of the plain attention (gpu_helpers), whose arithmetic is the same: P, dS and
 the outputs are rounded to bf16 (relative error up to 2^-8 each, 2^-8 / sqrt(3) in the norm), and
-the cap adds an fp32 tanh: in the polynomial 1e-7 relative, in the exact form 1 - 2 / (1 + e^2u)
-an absolute error below 4e-7, so a score is off by at most 4e-7 c, LSE by as much: 1e-3 holds up to
-c = 2500, where no score of these inputs leaves the polynomial's range. Gradients with a cap can
+the cap adds an fp32 tanh: by polynomials up to |u| = 0.625 (4e-7 relative below 0.25, 1.1e-7
+above), and beyond in the form 1 - 2 / (1 + e^2u) with an absolute error below 4e-7, so a score is
+off by at most 4e-7 c, LSE by as much: 1e-3 holds up to c = 2500, where no score of these inputs
+leaves the polynomials' ranges. Gradients with a cap can
 be small where most scores sit on it (1 - tanh^2); the error of 1 - tanh^2 is below 1e-6, far
 below the bf16 rounding of what remains unless the factor itself is below 1e-4."""
 import ctypes
