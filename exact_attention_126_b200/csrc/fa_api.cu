@@ -867,7 +867,7 @@ const char* fa_status_string(fa_status_t status) {
 fa_status_t fa_debug_status(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
   // every kernel unit has its own copy of the status word: read and clear them all
-  const int words[17] = {fa_host::take_status_fwd64(),  fa_host::take_status_fwd128(),
+  const int words[18] = {fa_host::take_status_fwd64(),  fa_host::take_status_fwd128(),
                         fa_host::take_status_bwd64(),  fa_host::take_status_bwd128(),
                         fa_host::take_status_fused64(), fa_host::take_status_fwdp64(),
                         fa_host::take_status_fwdp128(), fa_host::take_status_bwdp64(),
@@ -875,7 +875,7 @@ fa_status_t fa_debug_status(void* stream) {
                         fa_host::take_status_fwds128(), fa_host::take_status_fwdsp64(),
                         fa_host::take_status_fwdsp128(), fa_host::take_status_bwds64(),
                         fa_host::take_status_bwds128(), fa_host::take_status_bwdsp64(),
-                        fa_host::take_status_bwdsp128()};
+                        fa_host::take_status_bwdsp128(), fa_host::take_status_rope()};
   bool timeout = false;
   for (int w : words) {
     if (w < 0) return FA_ERR_CUDA;

@@ -3,11 +3,14 @@
 #include <atomic>
 
 #include "fa_rope.cuh"
+#include "tma_maps.h"
 #include "launch.h"
 
 namespace fa_host {
 
 namespace {
+
+constexpr long long kTileMinBytes = 16ll << 20;
 
 // SMs of the current device (asked once per device).
 int device_sms() {
@@ -39,8 +42,70 @@ int plan(fa::RopeArgs& a, int d) {
   return (int)(blocks < most ? blocks : most);
 }
 
+// The tensor map of rows of one kind as the tile kernel takes them: (d, N, heads, B) boxes of
+// kHeads heads x kTokens tokens. False where no map can be made of them (rows shared through a
+// stride of 0, strides past the copy engine's).
+bool rows_map(CUtensorMap* map, const fa::HeadRows& r, const fa::RopeArgs& a, int d, int tokens,
+              int heads) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const bool packed = a.cu != nullptr;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)(packed ? a.tokens : a.N),
+                              (cuuint64_t)r.heads, (cuuint64_t)(packed ? 1 : a.B)};
+  cuuint64_t strides[3] = {(cuuint64_t)r.sn * 2, (cuuint64_t)r.sh * 2, (cuuint64_t)r.sb * 2};
+  for (int i = 0; i < 3; ++i) {
+    if (dims[i + 1] == 1) strides[i] = (cuuint64_t)d * 2;  // never stepped
+    if (strides[i] == 0 || strides[i] >= (1ull << 40)) return false;
+  }
+  const cuuint32_t box[4] = {(cuuint32_t)d, (cuuint32_t)tokens, (cuuint32_t)heads, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, r.data, dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Launches the tile kernel if the problem is one for it: sequences of at least a tile of tokens
+// and enough rows to fill every block several times over (below that the ring never fills and
+// the first tile's latency is the time; TILE_RULE). Returns its blocks, 0 if it was not launched, -1 on
+// an error.
+template <int D, bool kInter, bool kBwd>
+int tiles(const fa::RopeArgs& a, cudaStream_t st) {
+  using T = fa::RopeTile<D, kBwd>;
+  const int sms = device_sms();
+  const int rows = a.cu != nullptr ? a.tokens : a.N;
+  long long bytes = 0, items = 0;
+  const long long per_kind =
+      ((long long)rows + T::kTokens - 1) / T::kTokens * (a.cu != nullptr ? 1 : a.B);
+  for (const fa::HeadRows& y : a.y) {
+    bytes += (long long)a.tokens * y.heads * D * 2;
+    if (y.heads > 0) items += per_kind;
+  }
+  if (rows < T::kTokens || bytes < kTileMinBytes) return 0;
+  fa::RopeMaps m;
+  for (int i = 0; i < 3; ++i) {
+    if (a.y[i].heads == 0) continue;
+    const bool ok = rows_map(&m.in[i], kBwd ? a.y[i] : a.x[i], a, D, T::kTokens, T::kHeads) &&
+                    rows_map(&m.out[i], kBwd ? a.g[i] : a.y[i], a, D, T::kTokens, T::kHeads) &&
+                    (!kBwd || i == 2 || !a.norm ||
+                     rows_map(&m.x[i], a.x[i], a, D, T::kTokens, T::kHeads));
+    if (!ok) return 0;
+  }
+  if (cudaFuncSetAttribute(fa::fa_rope_tile_kernel<D, kInter, kBwd>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           T::kSmemBytes) != cudaSuccess)
+    return -1;
+  long long grid = (long long)sms * fa::kRopeBlocksPerSm;
+  if (grid > items) grid = items;
+  if (grid > fa::kRopeMaxBlocks) grid = fa::kRopeMaxBlocks;
+  fa::fa_rope_tile_kernel<D, kInter, kBwd>
+      <<<(unsigned)grid, T::kThreads, T::kSmemBytes, st>>>(m, a);
+  return status() == FA_OK ? (int)grid : -1;
+}
+
 template <int D, bool kInter>
 fa_status_t fwd(fa::RopeArgs a, cudaStream_t st) {
+  const int tiled = tiles<D, kInter, false>(a, st);
+  if (tiled != 0) return tiled > 0 ? FA_OK : FA_ERR_CUDA;
   const int grid = plan(a, D);
   fa::fa_rope_fwd_kernel<D, kInter><<<grid, fa::kRopeThreads, 0, st>>>(a);
   return status();
@@ -50,6 +115,10 @@ template <int D, bool kInter>
 fa_status_t bwd(fa::RopeArgs a, cudaStream_t st) {
   int blocks = 0;
   if (a.tokens > 0) {
+    blocks = tiles<D, kInter, true>(a, st);
+    if (blocks < 0) return FA_ERR_CUDA;
+  }
+  if (a.tokens > 0 && blocks == 0) {
     blocks = plan(a, D);
     if (blocks > fa::kRopeMaxBlocks) blocks = fa::kRopeMaxBlocks;
     fa::fa_rope_bwd_kernel<D, kInter><<<blocks, fa::kRopeThreads, 0, st>>>(a);
@@ -62,6 +131,16 @@ fa_status_t bwd(fa::RopeArgs a, cudaStream_t st) {
 }
 
 }  // namespace
+
+int take_status_rope() {
+  int v = 0;
+  if (cudaMemcpyFromSymbol(&v, fa::g_fa_status, sizeof(int)) != cudaSuccess) return -1;
+  if (v != 0) {
+    const int zero = 0;
+    if (cudaMemcpyToSymbol(fa::g_fa_status, &zero, sizeof(int)) != cudaSuccess) return -1;
+  }
+  return v;
+}
 
 fa_status_t launch_rope_fwd(const fa::RopeArgs& a, int d, bool interleaved, cudaStream_t st) {
   if (d == 64) return interleaved ? fwd<64, true>(a, st) : fwd<64, false>(a, st);

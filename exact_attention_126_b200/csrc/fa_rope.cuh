@@ -170,20 +170,15 @@ struct RopeTurns {
     }
   }
 
-  // Writes the cosine and sine of each of the token's rotations to `cs` (this warp's D / 2
-  // entries of shared memory) and loads those of this lane's pairs.
-  template <typename Lane>
-  __device__ __forceinline__ void compute(const RopeArgs& a, const RopeToken& k, int t,
-                                          const Lane& ln, float2* cs, float2 (&c)[2],
-                                          float2 (&s)[2]) const {
-    if (a.rot == 0) return;
-    __syncwarp();  // the previous token's entries have been read
+  // Writes the cosine and sine of each rotation of token t (the place-th of its sequence) to `cs`
+  // (D / 2 entries of shared memory); by all lanes of the warp.
+  __device__ __forceinline__ void fill(const RopeArgs& a, int place, int t, float2* cs) const {
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
       const int p = (threadIdx.x & 31) + 32 * i;
       if (p < a.rot / 2) {
         const long long pos =
-            a.positions != nullptr ? __ldg(a.positions + (size_t)axis[i] * a.tokens + t) : k.place;
+            a.positions != nullptr ? __ldg(a.positions + (size_t)axis[i] * a.tokens + t) : place;
         const unsigned long long ph = (unsigned long long)pos * turn[i];
         // the top 32 bits as a signed fraction of a turn, in half turns
         float sn, cn;
@@ -191,16 +186,31 @@ struct RopeTurns {
         cs[p] = make_float2(cn, sn);
       }
     }
-    __syncwarp();
-    if (ln.turns) {
-      const float4* src = reinterpret_cast<const float4*>(cs + 4 * ln.chunk);
+  }
+
+  // Loads those of this lane's pairs.
+  template <typename Lane>
+  __device__ __forceinline__ void read(const Lane& ln, const float2* cs, float2 (&c)[2],
+                                       float2 (&s)[2]) const {
+    if (!ln.turns) return;
+    const float4* src = reinterpret_cast<const float4*>(cs + 4 * ln.chunk);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 v = src[i];
-        c[i] = make_float2(v.x, v.z);
-        s[i] = make_float2(v.y, v.w);
-      }
+    for (int i = 0; i < 2; ++i) {
+      const float4 v = src[i];
+      c[i] = make_float2(v.x, v.z);
+      s[i] = make_float2(v.y, v.w);
     }
+  }
+
+  template <typename Lane>
+  __device__ __forceinline__ void compute(const RopeArgs& a, const RopeToken& k, int t,
+                                          const Lane& ln, float2* cs, float2 (&c)[2],
+                                          float2 (&s)[2]) const {
+    if (a.rot == 0) return;
+    __syncwarp();  // the previous token's entries have been read
+    fill(a, k.place, t, cs);
+    __syncwarp();
+    read(ln, cs, c, s);
   }
 };
 
@@ -465,8 +475,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) fa_rope_bwd_ke
                 gx.f[j] = __fmul2_rn(d.f[j], p.f[j]);
                 sx = __ffma2_rn(gx.e[j], w.e[j], __ffma2_rn(gx.f[j], w.f[j], sx));
               }
-              // (rows of no head hold zeros: they add nothing)
-              const float rs = rsqrtf(row_sum<D>(ss.x + ss.y) * (1.f / D) + a.eps);
+              float rs = rsqrtf(row_sum<D>(ss.x + ss.y) * (1.f / D) + a.eps);
+              // (rows of no head add nothing, also with eps = 0)
+              if (sh.head + (u + i) * stride >= heads) rs = 0.f;
               const float2 m = both(row_sum<D>(sx.x + sx.y) * rs * rs * (-1.f / D));
               const float2 r2 = both(rs);
               Pairs& sum = acc[part < 2 ? part : 0];
@@ -513,6 +524,376 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) fa_rope_bwd_ke
     float v = 0.f;
 #pragma unroll
     for (int q = 0; q < kRopeWarps; ++q) v += (&sums[q][0][0])[i];
+    a.partial[(size_t)blockIdx.x * 2 * D + i] = v;
+  }
+}
+
+// ------------------------------------------------------------------------------ tiles
+// The same two computations on large problems, through shared memory: a tile is kTileTokens
+// consecutive tokens of kTileHeads heads of one kind, [head][token][D], which the copy engine
+// fetches from and puts to tensors of any strides. One thread issues the loads of a ring of
+// stages, eight warps work on a full stage in place, and one thread issues the stores of the
+// finished ones, so that loads and stores run while other stages are worked on, whatever the
+// latency. A warp owns kRows tokens of each tile, one row per D / 8 lanes, and steps through the
+// heads: cosines, sines and the gain stay in registers. Items (all heads of a kind for a tile of
+// tokens) go queries first, then keys, then values, dealt to persistent blocks.
+//   B32 N2048 3 x 16 heads of 64: forward TIME_F, backward TIME_B (kernels above 167 and 249 us)
+struct RopeMaps {
+  CUtensorMap in[3];   // forward: x; backward: the incoming gradients y
+  CUtensorMap out[3];  // forward: y; backward: g
+  CUtensorMap x[2];    // backward with norm: x
+};
+
+template <int D, bool kBwd>
+struct RopeTile {
+  static constexpr int kRows = 32 / (D / 8);          // tokens of a warp
+  static constexpr int kTokens = kRows * kRopeWarps;  // 32 (D = 64) or 16
+  static constexpr int kHeads = 4;
+  static constexpr int kBytes = kHeads * kTokens * D * 2;  // 16 KB
+  static constexpr int kStage = kBwd ? 2 * kBytes : kBytes;
+  static constexpr int kStages = kBwd ? 3 : 6;
+  static constexpr int kThreads = kRopeThreads + 64;  // eight working warps, load warp, store warp
+  static constexpr int kBar = kStages * kStage;       // full, done, empty barriers
+  static constexpr int kMisc = (kBar + 3 * kStages * 8 + 15) / 16 * 16;
+  static constexpr int kCs = kMisc + 16;              // cosines and sines of each warp's tokens
+  static constexpr int kSums = kCs + kRopeWarps * kRows * (D / 2) * 8;
+  static_assert(kCs % 16 == 0, "float4 loads of the cosines and sines");
+  static constexpr int kSmemBytes = kSums + (kBwd ? kRopeWarps * 2 * D * 4 : 0) + 128;
+};
+
+// The items of a call: tiles of tokens per kind.
+struct RopeItems {
+  int per_entry;  // tiles of an entry's N rows (packed: of the tensor)
+  int tiles;
+  int ends[3];    // items of queries, of queries and keys, of all
+};
+
+template <int kTokens>
+__device__ __forceinline__ RopeItems rope_items(const RopeArgs& a, const HeadRows (&y)[3]) {
+  RopeItems r;
+  const int rows = a.cu != nullptr ? a.tokens : a.N;
+  r.per_entry = (rows + kTokens - 1) / kTokens;
+  r.tiles = a.cu != nullptr ? r.per_entry : r.per_entry * a.B;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    if (y[i].heads > 0) n += r.tiles;
+    r.ends[i] = n;
+  }
+  return r;
+}
+
+// Item `it`: kind, entry, first row (n0 of entry b) and steps of kHeads heads.
+struct RopeItem {
+  int part, b, n0, steps;
+};
+template <int kTokens, int kHeads>
+__device__ __forceinline__ RopeItem rope_item(const RopeItems& r, const HeadRows (&y)[3], int it) {
+  RopeItem k;
+  k.part = it < r.ends[0] ? 0 : (it < r.ends[1] ? 1 : 2);
+  const int t = it - (k.part == 0 ? 0 : r.ends[k.part - 1]);
+  k.b = t / r.per_entry;
+  k.n0 = (t - k.b * r.per_entry) * kTokens;
+  k.steps = (y[k.part].heads + kHeads - 1) / kHeads;
+  return k;
+}
+
+// The token of row n0 + lane of an item's tile, for lanes below kTokens; `whole` (warp-wide):
+// every row of the tile inside the tensor is one the call writes, so that the tile leaves as one.
+template <int kTokens>
+__device__ __forceinline__ RopeToken tile_token(const RopeArgs& a, const RopeItem& k, bool& whole) {
+  const int lane = threadIdx.x & 31;
+  const int n = k.n0 + (lane < kTokens ? lane : 0);
+  RopeToken t;
+  if (a.cu != nullptr) {
+    t = rope_token(a, n < a.tokens ? n : a.tokens - 1);
+    if (n >= a.tokens) t.live = t.owned = false;
+    whole = __all_sync(0xffffffffu, t.owned || n >= a.tokens);
+  } else {
+    t.b = k.b;
+    t.n = t.place = n;
+    t.owned = n < a.N;
+    t.live = t.owned && (a.seq_len == nullptr || n < __ldg(a.seq_len + k.b));
+    whole = true;
+  }
+  return t;
+}
+
+// A lane's eight values of a row in shared memory at `p` (bytes). At D = 64 the four rows of a
+// warp lie 128 bytes apart: rows of odd `sub` take their two halves in the other order, so that
+// the lanes of a wavefront meet different banks.
+template <int D, bool kInter, typename Lane>
+__device__ __forceinline__ RopeRaw tile_load(const uint8_t* p, const Lane& ln) {
+  RopeRaw r;
+  if (kInter) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p + 16 * ln.chunk);
+    r.a = make_uint2(v.x, v.y);
+    r.b = make_uint2(v.z, v.w);
+  } else {
+    const bool swap = D == 64 && (ln.sub & 1);
+    const uint2 u = *reinterpret_cast<const uint2*>(p + 2 * (swap ? ln.ob : ln.oa));
+    const uint2 v = *reinterpret_cast<const uint2*>(p + 2 * (swap ? ln.oa : ln.ob));
+    r.a = swap ? v : u;
+    r.b = swap ? u : v;
+  }
+  return r;
+}
+template <int D, bool kInter, typename Lane>
+__device__ __forceinline__ void tile_store(uint8_t* p, const Lane& ln, const RopeRaw& r) {
+  if (kInter) {
+    *reinterpret_cast<uint4*>(p + 16 * ln.chunk) = make_uint4(r.a.x, r.a.y, r.b.x, r.b.y);
+  } else {
+    const bool swap = D == 64 && (ln.sub & 1);
+    *reinterpret_cast<uint2*>(p + 2 * (swap ? ln.ob : ln.oa)) = swap ? r.b : r.a;
+    *reinterpret_cast<uint2*>(p + 2 * (swap ? ln.oa : ln.ob)) = swap ? r.a : r.b;
+  }
+}
+
+template <int D, bool kInter, bool kBwd>
+__global__ void __launch_bounds__(RopeTile<D, kBwd>::kThreads, kRopeBlocksPerSm)
+    fa_rope_tile_kernel(const __grid_constant__ RopeMaps maps, const RopeArgs a) {
+  using T = RopeTile<D, kBwd>;
+  using L = RopeLane<D, kInter>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
+                                             ~uintptr_t(127));
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + T::kMisc);
+  auto full = [&](int s) -> uint32_t { return sb + T::kBar + 8u * s; };
+  auto done = [&](int s) -> uint32_t { return sb + T::kBar + 8u * (T::kStages + s); };
+  auto empty = [&](int s) -> uint32_t { return sb + T::kBar + 8u * (2 * T::kStages + s); };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < T::kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(done(s), kRopeWarps);
+      mbar_init(empty(s), 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (kBwd)
+    for (int i = threadIdx.x; i < kRopeWarps * 2 * D; i += T::kThreads)
+      reinterpret_cast<float*>(smem + T::kSums)[i] = 0.f;
+  __syncthreads();
+  const RopeItems items = rope_items<T::kTokens>(a, a.y);
+
+  if (warp == kRopeWarps) {
+    // ------------------------------------------------------------------ loads
+    if (lane == 0) {
+      int n = 0;
+      bool ok = true;
+      for (int it = blockIdx.x; ok && it < items.ends[2]; it += gridDim.x) {
+        const RopeItem k = rope_item<T::kTokens, T::kHeads>(items, a.y, it);
+        const bool with_x = kBwd && k.part < 2 && a.norm;
+        for (int g = 0; g < k.steps; ++g, ++n) {
+          const int s = n % T::kStages;
+          if (!mbar_wait(empty(s), ((n / T::kStages) & 1) ^ 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = sb + s * T::kStage;
+          mbar_arrive_expect_tx(full(s), with_x ? 2 * T::kBytes : T::kBytes);
+          tma_load_4d(dst, &maps.in[k.part], full(s), 0, k.n0, g * T::kHeads, k.b);
+          if (with_x)
+            tma_load_4d(dst + T::kBytes, &maps.x[k.part < 2 ? k.part : 0], full(s), 0, k.n0,
+                        g * T::kHeads, k.b);
+        }
+      }
+      // Drain: every copy issued must have landed before the block may exit.
+      for (int s = 0; s < T::kStages; ++s)
+        if (n > s) mbar_wait(full(s), ((n - 1 - s) / T::kStages) & 1, nullptr);
+    }
+  } else if (warp == kRopeWarps + 1) {
+    // ------------------------------------------------------------------ stores
+    int n = 0;
+    bool ok = true;
+    for (int it = blockIdx.x; ok && it < items.ends[2]; it += gridDim.x) {
+      const RopeItem k = rope_item<T::kTokens, T::kHeads>(items, a.y, it);
+      bool whole;
+      tile_token<T::kTokens>(a, k, whole);
+      for (int g = 0; g < k.steps; ++g, ++n) {
+        const int s = n % T::kStages;
+        if (!mbar_wait_warp(done(s), (n / T::kStages) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          // (the rows of a tile that does not leave as one were written by the working warps)
+          if (whole)
+            tma_store_4d(&maps.out[k.part], sb + s * T::kStage, 0, k.n0, g * T::kHeads, k.b);
+          bulk_commit();
+          // the previous stage's store has read it: its stage is free
+          bulk_wait_read_but_one();
+          if (n > 0) mbar_arrive(empty((n - 1) % T::kStages));
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+  } else {
+    // ------------------------------------------------------------------ working warps
+    const L ln(a);
+    const RopeTurns<D> turns(a);
+    float2* const cs = reinterpret_cast<float2*>(smem + T::kCs) + warp * (T::kRows * (D / 2));
+    const int mine = warp * T::kRows + ln.sub;  // this lane's token of a tile
+    Pairs w, acc;
+    int last_part = -1;
+    auto flush = [&]() {
+      // the gain's gradient over this warp's rows of one kind
+      if (!kBwd || last_part < 0 || last_part > 1 || a.partial == nullptr) return;
+      float* sums = reinterpret_cast<float*>(smem + T::kSums) + (warp * 2 + last_part) * D;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float e = j & 1 ? acc.e[j / 2].y : acc.e[j / 2].x;
+        float f = j & 1 ? acc.f[j / 2].y : acc.f[j / 2].x;
+#pragma unroll
+        for (int off = L::kLanes; off < 32; off <<= 1) {
+          e += __shfl_xor_sync(0xffffffffu, e, off);
+          f += __shfl_xor_sync(0xffffffffu, f, off);
+        }
+        if (ln.sub == 0) {
+          sums[ln.col_e(j)] = e;
+          sums[ln.col_f(j)] = f;
+        }
+      }
+    };
+    int n = 0;
+    bool ok = true;
+    for (int it = blockIdx.x; ok && it < items.ends[2]; it += gridDim.x) {
+      const RopeItem k = rope_item<T::kTokens, T::kHeads>(items, a.y, it);
+      bool whole;
+      const RopeToken t = tile_token<T::kTokens>(a, k, whole);
+      const bool live = __shfl_sync(0xffffffffu, (int)t.live, mine) != 0;
+      const bool owned = __shfl_sync(0xffffffffu, (int)t.owned, mine) != 0;
+      const int heads = a.y[k.part].heads;
+      if (k.part != last_part) {
+        flush();
+        last_part = k.part;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          acc.e[j] = acc.f[j] = both(0.f);
+          w.e[j] = w.f[j] = both(1.f);
+          const float* gain = k.part < 2 && a.norm ? a.w[k.part] : nullptr;
+          if (gain != nullptr) {
+            w.e[j] = make_float2(__ldg(gain + ln.col_e(2 * j)), __ldg(gain + ln.col_e(2 * j + 1)));
+            w.f[j] = make_float2(__ldg(gain + ln.col_f(2 * j)), __ldg(gain + ln.col_f(2 * j + 1)));
+          }
+        }
+      }
+      float2 c[2], s[2], ns[2];
+      if (k.part < 2 && a.rot > 0) {
+        __syncwarp();  // the previous item's entries have been read
+#pragma unroll
+        for (int j = 0; j < T::kRows; ++j) {
+          const int place = __shfl_sync(0xffffffffu, t.place, warp * T::kRows + j);
+          const int row = k.n0 + warp * T::kRows + j;
+          const int at = a.cu != nullptr ? row : k.b * a.N + row;
+          if (row < (a.cu != nullptr ? a.tokens : a.N))
+            turns.fill(a, place, at, cs + j * (D / 2));
+        }
+        __syncwarp();
+        turns.read(ln, cs + ln.sub * (D / 2), c, s);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) ns[j] = make_float2(-s[j].x, -s[j].y);
+      }
+      for (int g = 0; g < k.steps; ++g, ++n) {
+        const int st = n % T::kStages;
+        if (!mbar_wait_warp(full(st), (n / T::kStages) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        uint8_t* const p0 = smem + st * T::kStage + mine * (D * 2);
+#pragma unroll
+        for (int hh = 0; hh < T::kHeads; ++hh) {
+          if (g * T::kHeads + hh >= heads) break;
+          uint8_t* const row = p0 + hh * (T::kTokens * D * 2);
+          if (k.part == 2 && whole && live) continue;  // values stay as they came
+          RopeRaw r = tile_load<D, kInter>(row, ln);
+          if (k.part < 2) {
+            Pairs v = unpack_pairs<kInter>(r);
+            if (!kBwd) {
+              if (a.norm) {
+                float2 ss = __fmul2_rn(v.e[0], v.e[0]);
+                ss = __ffma2_rn(v.e[1], v.e[1], ss);
+                ss = __ffma2_rn(v.f[0], v.f[0], ss);
+                ss = __ffma2_rn(v.f[1], v.f[1], ss);
+                const float2 rs = both(rsqrtf(row_sum<D>(ss.x + ss.y) * (1.f / D) + a.eps));
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  v.e[j] = __fmul2_rn(__fmul2_rn(v.e[j], rs), w.e[j]);
+                  v.f[j] = __fmul2_rn(__fmul2_rn(v.f[j], rs), w.f[j]);
+                }
+              }
+              if (ln.turns) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  const float2 e = v.e[j], f = v.f[j];
+                  v.e[j] = __ffma2_rn(f, ns[j], __fmul2_rn(e, c[j]));
+                  v.f[j] = __ffma2_rn(e, s[j], __fmul2_rn(f, c[j]));
+                }
+              }
+            } else {
+              if (ln.turns) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  const float2 e = v.e[j], f = v.f[j];
+                  v.e[j] = __ffma2_rn(f, s[j], __fmul2_rn(e, c[j]));
+                  v.f[j] = __ffma2_rn(e, ns[j], __fmul2_rn(f, c[j]));
+                }
+              }
+              if (a.norm) {
+                const Pairs x = unpack_pairs<kInter>(tile_load<D, kInter>(row + T::kBytes, ln));
+                float2 ss = __fmul2_rn(x.e[0], x.e[0]);
+                ss = __ffma2_rn(x.e[1], x.e[1], ss);
+                ss = __ffma2_rn(x.f[0], x.f[0], ss);
+                ss = __ffma2_rn(x.f[1], x.f[1], ss);
+                Pairs gx;  // g o x: the gain's gradient up to the row's r
+                float2 sx = both(0.f);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  gx.e[j] = __fmul2_rn(v.e[j], x.e[j]);
+                  gx.f[j] = __fmul2_rn(v.f[j], x.f[j]);
+                  sx = __ffma2_rn(gx.e[j], w.e[j], __ffma2_rn(gx.f[j], w.f[j], sx));
+                }
+                const float rs = rsqrtf(row_sum<D>(ss.x + ss.y) * (1.f / D) + a.eps);
+                const float2 m = both(row_sum<D>(sx.x + sx.y) * rs * rs * (-1.f / D));
+                const float2 r2 = both(rs);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  if (live) {  // (rows past a length add nothing)
+                    acc.e[j] = __ffma2_rn(gx.e[j], r2, acc.e[j]);
+                    acc.f[j] = __ffma2_rn(gx.f[j], r2, acc.f[j]);
+                  }
+                  v.e[j] = __fmul2_rn(__ffma2_rn(x.e[j], m, __fmul2_rn(v.e[j], w.e[j])), r2);
+                  v.f[j] = __fmul2_rn(__ffma2_rn(x.f[j], m, __fmul2_rn(v.f[j], w.f[j])), r2);
+                }
+              }
+            }
+            r = pack_pairs<kInter>(v);
+          }
+          if (!live) r.a = r.b = make_uint2(0, 0);
+          tile_store<D, kInter>(row, ln, r);
+          if (!whole && owned) {
+            const HeadRows& o = kBwd ? a.g[k.part] : a.y[k.part];
+            const RopeToken tok{0, k.n0 + mine, 0, true, true};
+            store_row<kInter>(walk_rows(o, tok, g * T::kHeads + hh, 1).p, ln, r);
+          }
+        }
+        fence_async_smem();
+        mbar_arrive_warp(done(st));
+      }
+    }
+    flush();
+  }
+  __syncthreads();
+  if (!kBwd || a.partial == nullptr) return;
+  const float* sums = reinterpret_cast<const float*>(smem + T::kSums);
+  for (int i = threadIdx.x; i < 2 * D; i += T::kThreads) {
+    float v = 0.f;
+#pragma unroll
+    for (int q = 0; q < kRopeWarps; ++q) v += sums[q * 2 * D + i];
     a.partial[(size_t)blockIdx.x * 2 * D + i] = v;
   }
 }

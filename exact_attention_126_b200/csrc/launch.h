@@ -110,6 +110,7 @@ int take_status_bwdp128();
 int take_status_bwd64();
 int take_status_bwd128();
 int take_status_fused64();
+int take_status_rope();
 int take_status_fwds64();
 int take_status_fwds128();
 int take_status_fwdsp64();

@@ -12,29 +12,11 @@
 #include "fa_bwd_fused.cuh"
 #include "fa_fwd.cuh"
 #include "launch.h"
+#include "tma_maps.h"
 
 namespace fa_host {
 
 using fa::kBlock;
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's cuTensorMapEncodeTiled, looked up once (thread-safe static initialisation).
-inline EncodeTiledFn encode_fn() {
-  static const EncodeTiledFn fn = []() -> EncodeTiledFn {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      return reinterpret_cast<EncodeTiledFn>(p);
-    return nullptr;
-  }();
-  return fn;
-}
 
 // The fused backward's dQ accumulator: (B*H, Np, 64) fp32, boxes of 32 columns (128 bytes)
 // x 128 rows, 128-byte swizzle.

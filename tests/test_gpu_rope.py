@@ -186,6 +186,9 @@ def test_rows_of_uneven_size():
     x, kw = make((2, 40), (4, 4, 1), 128, 128, 1, spread=True)
     check(x, (4, 4, 1), kw)
     check(x, (4, 4, 1), kw, eps=0.0)
+    x, kw = make((1, 5), (3, 5, 1), 64, 64, 1)  # rows of a step that hold no head
+    check(x, (3, 5, 1), kw, eps=0.0)
+    x, kw = make((2, 40), (4, 4, 1), 128, 128, 1, spread=True)
     x[0, 3] = 0  # a row of zeros: 0 / sqrt(eps)
     check(x, (4, 4, 1), kw)
 
@@ -196,6 +199,95 @@ def test_many_tokens():
     check(x, (6, 2, 2), kw)
     x, kw = make((1, 9001), (2, 1, 1), 128, 64, 2)
     check(x, (2, 1, 1), kw, True)
+
+
+# Large problems go through tiles of tokens (32 at d 64, 16 at d 128) by heads (4): odd numbers of
+# both, heads that share a tile with none, several tiles per block.
+@pytest.mark.parametrize("d,heads", [(64, (9, 3, 3)), (128, (5, 2, 1))])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rot,axes,norm", [(None, 1, True), (24, 3, True), (0, 1, True),
+                                           (None, 2, False)])
+def test_tiles(d, heads, interleaved, rot, axes, norm):
+    x, kw = make((5, 3001), heads, d, d if rot is None else rot, axes, gains=norm)
+    check(x, heads, kw, interleaved, norm=norm)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_tiles_of_a_padded_batch(d):
+    B, N, heads = 7, 2222, (6, 5, 4)
+    x, kw = make((B, N), heads, d, d, 1)
+    lens = [2222, 0, 33, 1, 5000, 2048, 1000]
+    live = (np.arange(N) < np.array(lens)[:, None]).reshape(-1)
+    x[torch.from_numpy(~live.reshape(B, N))] = float("nan")
+    check(x, heads, kw, live=live, eps=0.0,
+          seq_lengths=torch.tensor(lens, dtype=torch.int32, device=x.device))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("given", [False, True])
+def test_tiles_of_a_packed_batch(d, given):
+    lens, first, total, N = [5, 0, 6400, 1, 0, 9000, 700, 0], 37, 16300, 8000
+    heads = (6, 3, 5)
+    cu = first + np.concatenate([[0], np.cumsum(lens)])
+    x, kw = make((total,), heads, d, d, 1, positions="near" if given else None)
+    live, places = np.zeros(total, bool), np.zeros(total)
+    for b, n in enumerate(lens):
+        live[cu[b]:cu[b] + min(n, N)] = True
+        places[cu[b]:cu[b] + n] = np.arange(n)
+    x[torch.from_numpy(~live)] = float("inf")
+    call = dict(cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=x.device), max_seqlen=N)
+    check(x, heads, kw, live=live, places=places, **call)
+    # in place, and rows that no sequence covers stay as they were
+    q, k, v = x.split(heads, -2)
+    ref = fa.qk_norm_rope_forward(q, k, v, **kw, **call)
+    y = x.clone()
+    B, N, params = fa._norm_rope_params(y.device, (total,), d, kw["q_weight"], kw["k_weight"],
+                                        1e-6, True, kw["inv_freq"], kw.get("positions"), None,
+                                        False, None, call["cu_seqlens"], N)
+    parts = [fa._rows(t, "x", (total,), d, y.device, 1) for t in y.split(heads, 1)]
+    fa.fa_qk_norm_rope_fwd(*parts, *parts, B, N, d, params)
+    for a, b in zip(y.split(heads, 1), ref):
+        assert torch.equal(a.cpu()[torch.from_numpy(live)], b.cpu()[torch.from_numpy(live)])
+    assert torch.isinf(y.cpu()[torch.from_numpy(~live)]).all()
+
+
+def test_tiles_and_rows_agree():
+    """A stride of 0 (shared rows) keeps a call out of the tiles: the same values either way; and
+    repeats, streams and a graph of the tile kernels."""
+    dev = torch.device("cuda:0")
+    x, kw = make((4, 2500), (8, 1, 4), 64, 64, 1)
+    q, k, v = x.split((8, 1, 4), 2)
+    k4 = k.expand(4, 2500, 4, 64)
+    a = fa.qk_norm_rope_forward(q, k4, v, **kw)
+    b = fa.qk_norm_rope_forward(q, k4.contiguous(), v, **kw)
+    for s, t in zip(a, b):
+        # (the norm's sum in another order: at most one bf16 step apart)
+        assert (s.float() - t.float()).abs().max() <= 2.0 ** -7 * s.float().abs().max()
+        assert (s != t).float().mean() < 1e-3
+    dy = [torch.randn_like(t) for t in b]
+    kc = k4.contiguous()
+    ref = fa.qk_norm_rope_backward(*dy, q=q, k=kc, **kw)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    runs = []
+    for _ in range(4):
+        for s in (s1, s2):
+            with torch.cuda.stream(s):
+                runs.append(fa.qk_norm_rope_backward(*dy, q=q, k=kc, **kw))
+    torch.cuda.synchronize()
+    for r in runs:
+        assert all(torch.equal(m, n) for m, n in zip(r, ref))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = fa.qk_norm_rope_forward(q, kc, v, **kw)
+        grads = fa.qk_norm_rope_backward(*dy, q=q, k=kc, **kw)
+    for t in out + grads:
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(m, n) for m, n in zip(out, b))
+    assert all(torch.equal(m, n) for m, n in zip(grads, ref))
+    assert fa.fa_debug_status() == 0
 
 
 @pytest.mark.parametrize("d", [64, 128])
