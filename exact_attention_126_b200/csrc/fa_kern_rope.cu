@@ -10,7 +10,11 @@ namespace fa_host {
 
 namespace {
 
-constexpr long long kTileMinBytes = 16ll << 20;
+// From how many bytes of rows the tile kernel runs. Measured against the row kernels (d = 64, 3 x 16
+// heads / d = 128, 32 + 2 x 8 heads, one sequence): forward 18.4 us either way at 25 MB, 28.7 -> 24.6
+// / 28.7 -> 30.7 at 50 MB, 84 -> 76 / 82 -> 82 at 201 MB; backward 28.7 either way / 30 -> 33, 47 ->
+// 39 / 45 -> 44 and 133 -> 104 / 131 -> 119.
+constexpr long long kTileMinBytes = 32ll << 20;
 
 // SMs of the current device (asked once per device).
 int device_sms() {
@@ -64,10 +68,9 @@ bool rows_map(CUtensorMap* map, const fa::HeadRows& r, const fa::RopeArgs& a, in
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Launches the tile kernel if the problem is one for it: sequences of at least a tile of tokens
-// and enough rows to fill every block several times over (below that the ring never fills and
-// the first tile's latency is the time; TILE_RULE). Returns its blocks, 0 if it was not launched, -1 on
-// an error.
+// Launches the tile kernel if the problem is one for it: sequences of at least a tile of tokens,
+// kTileMinBytes of rows, strides that a tensor map takes. Returns its blocks, 0 if it was not
+// launched, -1 on an error.
 template <int D, bool kInter, bool kBwd>
 int tiles(const fa::RopeArgs& a, cudaStream_t st) {
   using T = fa::RopeTile<D, kBwd>;

@@ -537,7 +537,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) fa_rope_bwd_ke
 // latency. A warp owns kRows tokens of each tile, one row per D / 8 lanes, and steps through the
 // heads: cosines, sines and the gain stay in registers. Items (all heads of a kind for a tile of
 // tokens) go queries first, then keys, then values, dealt to persistent blocks.
-//   B32 N2048 3 x 16 heads of 64: forward TIME_F, backward TIME_B (kernels above 167 and 249 us)
+//   B32 N2048, 3 x 16 heads of 64: forward 143 us (805 MB, 5.6 TB/s), backward 193 us (1.07 GB,
+//   5.6 TB/s); the kernels above take 160 and 252 us. Bound by device memory: a plain copy runs at
+//   6.55 TB/s, rows of 128 bytes on one side cost the rest.
 struct RopeMaps {
   CUtensorMap in[3];   // forward: x; backward: the incoming gradients y
   CUtensorMap out[3];  // forward: y; backward: g
@@ -619,10 +621,10 @@ __device__ __forceinline__ RopeToken tile_token(const RopeArgs& a, const RopeIte
   return t;
 }
 
-// A lane's eight values of a row in shared memory at `p` (bytes). At D = 64 the four rows of a
-// warp lie 128 bytes apart: rows of odd `sub` take their two halves in the other order, so that
-// the lanes of a wavefront meet different banks.
-template <int D, bool kInter, typename Lane>
+// A lane's eight values of a row in shared memory at `p` (bytes). (At D = 64 the rows of a warp
+// lie 128 bytes apart and the halves of two rows meet in the same banks; taking them in turns costs
+// more instructions than it saves wavefronts: forward 145 -> 149 us on the problem above.)
+template <bool kInter, typename Lane>
 __device__ __forceinline__ RopeRaw tile_load(const uint8_t* p, const Lane& ln) {
   RopeRaw r;
   if (kInter) {
@@ -630,22 +632,18 @@ __device__ __forceinline__ RopeRaw tile_load(const uint8_t* p, const Lane& ln) {
     r.a = make_uint2(v.x, v.y);
     r.b = make_uint2(v.z, v.w);
   } else {
-    const bool swap = D == 64 && (ln.sub & 1);
-    const uint2 u = *reinterpret_cast<const uint2*>(p + 2 * (swap ? ln.ob : ln.oa));
-    const uint2 v = *reinterpret_cast<const uint2*>(p + 2 * (swap ? ln.oa : ln.ob));
-    r.a = swap ? v : u;
-    r.b = swap ? u : v;
+    r.a = *reinterpret_cast<const uint2*>(p + 2 * ln.oa);
+    r.b = *reinterpret_cast<const uint2*>(p + 2 * ln.ob);
   }
   return r;
 }
-template <int D, bool kInter, typename Lane>
+template <bool kInter, typename Lane>
 __device__ __forceinline__ void tile_store(uint8_t* p, const Lane& ln, const RopeRaw& r) {
   if (kInter) {
     *reinterpret_cast<uint4*>(p + 16 * ln.chunk) = make_uint4(r.a.x, r.a.y, r.b.x, r.b.y);
   } else {
-    const bool swap = D == 64 && (ln.sub & 1);
-    *reinterpret_cast<uint2*>(p + 2 * (swap ? ln.ob : ln.oa)) = swap ? r.b : r.a;
-    *reinterpret_cast<uint2*>(p + 2 * (swap ? ln.oa : ln.ob)) = swap ? r.a : r.b;
+    *reinterpret_cast<uint2*>(p + 2 * ln.oa) = r.a;
+    *reinterpret_cast<uint2*>(p + 2 * ln.ob) = r.b;
   }
 }
 
@@ -687,6 +685,8 @@ __global__ void __launch_bounds__(RopeTile<D, kBwd>::kThreads, kRopeBlocksPerSm)
       for (int it = blockIdx.x; ok && it < items.ends[2]; it += gridDim.x) {
         const RopeItem k = rope_item<T::kTokens, T::kHeads>(items, a.y, it);
         const bool with_x = kBwd && k.part < 2 && a.norm;
+        // a tile wholly past its entry's real length is only filled with zeros
+        const bool dead = a.seq_len != nullptr && k.n0 >= __ldg(a.seq_len + k.b);
         for (int g = 0; g < k.steps; ++g, ++n) {
           const int s = n % T::kStages;
           if (!mbar_wait(empty(s), ((n / T::kStages) & 1) ^ 1, abort_flag)) {
@@ -694,6 +694,10 @@ __global__ void __launch_bounds__(RopeTile<D, kBwd>::kThreads, kRopeBlocksPerSm)
             break;
           }
           const uint32_t dst = sb + s * T::kStage;
+          if (dead) {
+            mbar_arrive(full(s));  // nothing to fetch
+            continue;
+          }
           mbar_arrive_expect_tx(full(s), with_x ? 2 * T::kBytes : T::kBytes);
           tma_load_4d(dst, &maps.in[k.part], full(s), 0, k.n0, g * T::kHeads, k.b);
           if (with_x)
@@ -767,6 +771,7 @@ __global__ void __launch_bounds__(RopeTile<D, kBwd>::kThreads, kRopeBlocksPerSm)
       const RopeToken t = tile_token<T::kTokens>(a, k, whole);
       const bool live = __shfl_sync(0xffffffffu, (int)t.live, mine) != 0;
       const bool owned = __shfl_sync(0xffffffffu, (int)t.owned, mine) != 0;
+      const bool any_live = __any_sync(0xffffffffu, live);
       const int heads = a.y[k.part].heads;
       if (k.part != last_part) {
         flush();
@@ -810,8 +815,9 @@ __global__ void __launch_bounds__(RopeTile<D, kBwd>::kThreads, kRopeBlocksPerSm)
           if (g * T::kHeads + hh >= heads) break;
           uint8_t* const row = p0 + hh * (T::kTokens * D * 2);
           if (k.part == 2 && whole && live) continue;  // values stay as they came
-          RopeRaw r = tile_load<D, kInter>(row, ln);
-          if (k.part < 2) {
+          RopeRaw r = {};
+          if (any_live) r = tile_load<kInter>(row, ln);
+          if (k.part < 2 && any_live) {
             Pairs v = unpack_pairs<kInter>(r);
             if (!kBwd) {
               if (a.norm) {
@@ -844,7 +850,7 @@ __global__ void __launch_bounds__(RopeTile<D, kBwd>::kThreads, kRopeBlocksPerSm)
                 }
               }
               if (a.norm) {
-                const Pairs x = unpack_pairs<kInter>(tile_load<D, kInter>(row + T::kBytes, ln));
+                const Pairs x = unpack_pairs<kInter>(tile_load<kInter>(row + T::kBytes, ln));
                 float2 ss = __fmul2_rn(x.e[0], x.e[0]);
                 ss = __ffma2_rn(x.e[1], x.e[1], ss);
                 ss = __ffma2_rn(x.f[0], x.f[0], ss);
@@ -874,7 +880,7 @@ __global__ void __launch_bounds__(RopeTile<D, kBwd>::kThreads, kRopeBlocksPerSm)
             r = pack_pairs<kInter>(v);
           }
           if (!live) r.a = r.b = make_uint2(0, 0);
-          tile_store<D, kInter>(row, ln, r);
+          tile_store<kInter>(row, ln, r);
           if (!whole && owned) {
             const HeadRows& o = kBwd ? a.g[k.part] : a.y[k.part];
             const RopeToken tok{0, k.n0 + mine, 0, true, true};

@@ -208,15 +208,15 @@ def test_many_tokens():
 @pytest.mark.parametrize("rot,axes,norm", [(None, 1, True), (24, 3, True), (0, 1, True),
                                            (None, 2, False)])
 def test_tiles(d, heads, interleaved, rot, axes, norm):
-    x, kw = make((5, 3001), heads, d, d if rot is None else rot, axes, gains=norm)
+    x, kw = make((5, 3503), heads, d, d if rot is None else rot, axes, gains=norm)
     check(x, heads, kw, interleaved, norm=norm)
 
 
 @pytest.mark.parametrize("d", [64, 128])
 def test_tiles_of_a_padded_batch(d):
-    B, N, heads = 7, 2222, (6, 5, 4)
+    B, N, heads = 7, 2705, (6, 5, 4)
     x, kw = make((B, N), heads, d, d, 1)
-    lens = [2222, 0, 33, 1, 5000, 2048, 1000]
+    lens = [2705, 0, 33, 1, 5000, 2048, 1000]
     live = (np.arange(N) < np.array(lens)[:, None]).reshape(-1)
     x[torch.from_numpy(~live.reshape(B, N))] = float("nan")
     check(x, heads, kw, live=live, eps=0.0,
@@ -226,7 +226,7 @@ def test_tiles_of_a_padded_batch(d):
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("given", [False, True])
 def test_tiles_of_a_packed_batch(d, given):
-    lens, first, total, N = [5, 0, 6400, 1, 0, 9000, 700, 0], 37, 16300, 8000
+    lens, first, total, N = [5, 0, 6400, 1, 0, 9000, 3400, 0], 37, 19000, 8000
     heads = (6, 3, 5)
     cu = first + np.concatenate([[0], np.cumsum(lens)])
     x, kw = make((total,), heads, d, d, 1, positions="near" if given else None)
@@ -255,9 +255,9 @@ def test_tiles_and_rows_agree():
     """A stride of 0 (shared rows) keeps a call out of the tiles: the same values either way; and
     repeats, streams and a graph of the tile kernels."""
     dev = torch.device("cuda:0")
-    x, kw = make((4, 2500), (8, 1, 4), 64, 64, 1)
+    x, kw = make((4, 4200), (8, 1, 4), 64, 64, 1)
     q, k, v = x.split((8, 1, 4), 2)
-    k4 = k.expand(4, 2500, 4, 64)
+    k4 = k.expand(4, 4200, 4, 64)
     a = fa.qk_norm_rope_forward(q, k4, v, **kw)
     b = fa.qk_norm_rope_forward(q, k4.contiguous(), v, **kw)
     for s, t in zip(a, b):
