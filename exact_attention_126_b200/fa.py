@@ -175,10 +175,10 @@ def _shape(q: torch.Tensor, dims=None):
     """(B, H, N, d) of a (batch, heads, seq_len, head_dim) tensor, or `dims` as given (a
     packed batch's (total, heads, head_dim) tensors do not carry B and N)."""
     if dims is not None:
-        return tuple(int(x) for x in dims)
+        return tuple(map(int, dims))
     if q.dim() != 4:
         raise ValueError("expected a (batch, heads, seq_len, head_dim) tensor")
-    return tuple(int(x) for x in q.shape)
+    return tuple(q.shape)
 
 
 def _window(causal: bool, window) -> tuple[int, fa_window_t]:
@@ -428,14 +428,17 @@ def _scratch(nbytes, device, stream):
 
 
 def _check_inputs(*ts):
+    shape = ts[0].shape
     for t in ts:
         if not t.is_cuda:
             raise ValueError("tensors must be on a CUDA device")
-        if t.dtype != torch.bfloat16:
+        if t.dtype is not torch.bfloat16:
             raise ValueError("tensors must be bf16")
+        if t.get_device() != ts[0].get_device():
+            raise ValueError("tensors must be on one device")
         if not t.is_contiguous():
             raise ValueError("tensors must be contiguous (B, H, N, d)")
-        if t.shape != ts[0].shape:
+        if t.shape != shape:
             raise ValueError("q, k, v (and dO) must share one shape")
 
 
@@ -515,10 +518,10 @@ def attention_forward(q, k, v, scale=None, causal=False, window=(-1, -1), stream
     _check_inputs(q, k, v)
     if cu_seqlens is not None:
         B, H, N, d = _packed_dims(q, cu_seqlens, max_seqlen, seq_lengths)
-        lse = torch.empty((H, q.shape[0]), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((H, q.shape[0]), dtype=torch.float32)
     else:
         B, H, N, d = _shape(q)
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((B, H, N), dtype=torch.float32)
     o = torch.empty_like(q)
     o_low = torch.empty_like(q) if keep_residual else None
     if alibi_slopes is not None:
@@ -528,18 +531,19 @@ def attention_forward(q, k, v, scale=None, causal=False, window=(-1, -1), stream
     if seq_lengths is not None:
         _check_lengths(seq_lengths, q)
     score = _score(softcap, prefix_lengths, q, B)
-    if (alibi_slopes is None and key_padding is None and o_low is None and dropout is None
-            and seq_lengths is None and cu_seqlens is None and score is None):
-        fa_fwd(q, k, v, o, lse, scale, causal, window, stream)
-    else:
+    opt = None
+    if (alibi_slopes is not None or key_padding is not None or o_low is not None
+            or dropout is not None or seq_lengths is not None or cu_seqlens is not None):
         opt = options(alibi_slopes, key_padding, o_low, *(dropout or ()),
                       seq_lengths=seq_lengths, cu_seqlens=cu_seqlens,
                       total_tokens=q.shape[0] if cu_seqlens is not None else 0)
-        if score is None:
-            fa_fwd_ex(q, k, v, o, lse, opt, scale, causal, window, stream, dims=(B, H, N, d))
-        else:
-            fa_fwd_score(q, k, v, o, lse, opt, score, scale, causal, window, stream,
-                         dims=(B, H, N, d))
+    if score is not None:
+        fa_fwd_score(q, k, v, o, lse, opt, score, scale, causal, window, stream,
+                     dims=(B, H, N, d))
+    elif opt is not None:
+        fa_fwd_ex(q, k, v, o, lse, opt, scale, causal, window, stream, dims=(B, H, N, d))
+    else:
+        fa_fwd(q, k, v, o, lse, scale, causal, window, stream)
     return (o, lse, o_low) if keep_residual else (o, lse)
 
 
@@ -567,9 +571,6 @@ def attention_backward(q, k, v, o, lse, do, scale=None, causal=False, window=(-1
     dq = torch.empty_like(q)
     dk = torch.empty_like(q)
     dv = torch.empty_like(q)
-    ws = _scratch(fa_bwd_workspace_bytes_ex(
-        B, H, N, d, options(fused=fused, seq_lengths=seq_lengths, cu_seqlens=cu_seqlens,
-                            total_tokens=total)), q.device, stream)
     if alibi_slopes is not None:
         _check_slopes(alibi_slopes, q)
     if key_padding is not None:
@@ -579,19 +580,22 @@ def attention_backward(q, k, v, o, lse, do, scale=None, causal=False, window=(-1
     if seq_lengths is not None:
         _check_lengths(seq_lengths, q)
     score = _score(softcap, prefix_lengths, q, B)
-    if (alibi_slopes is None and key_padding is None and o_low is None and dropout is None
-            and not fused and seq_lengths is None and cu_seqlens is None and score is None):
-        fa_bwd(q, k, v, o, do, lse, dq, dk, dv, ws, scale, causal, window, stream)
-    else:
+    opt = None
+    if (alibi_slopes is not None or key_padding is not None or o_low is not None
+            or dropout is not None or fused or seq_lengths is not None
+            or cu_seqlens is not None):
         opt = options(alibi_slopes, key_padding, o_low, *(dropout or ()),
                       fused=fused, seq_lengths=seq_lengths, cu_seqlens=cu_seqlens,
                       total_tokens=total)
-        if score is None:
-            fa_bwd_ex(q, k, v, o, do, lse, dq, dk, dv, ws, opt, scale, causal, window, stream,
-                      dims=(B, H, N, d))
-        else:
-            fa_bwd_score(q, k, v, o, do, lse, dq, dk, dv, ws, opt, score, scale, causal, window,
-                         stream, dims=(B, H, N, d))
+    ws = _scratch(fa_bwd_workspace_bytes_ex(B, H, N, d, opt), q.device, stream)
+    if score is not None:
+        fa_bwd_score(q, k, v, o, do, lse, dq, dk, dv, ws, opt, score, scale, causal, window,
+                     stream, dims=(B, H, N, d))
+    elif opt is not None:
+        fa_bwd_ex(q, k, v, o, do, lse, dq, dk, dv, ws, opt, scale, causal, window, stream,
+                  dims=(B, H, N, d))
+    else:
+        fa_bwd(q, k, v, o, do, lse, dq, dk, dv, ws, scale, causal, window, stream)
     return dq, dk, dv
 
 
@@ -602,31 +606,28 @@ _BF16 = torch.bfloat16
 def _rows(t, name, tokens, d, device, heads_at):
     """The fa_heads_t of a bf16 tensor of any strides, token-major (B, N, heads, d), head-major
     (B, heads, N, d) (heads_at 2, 1) or packed (total, heads, d) (heads_at 1), checked to have
-    the given tokens and head_dim, d consecutive, on `device`; None for None."""
+    the given tokens and head_dim, d consecutive, on CUDA device number `device`; None for None."""
     if t is None:
         return None
-    shape, st = t.shape, t.stride()
-    if t.dtype != _BF16 or t.device != device:
+    if t.dtype is not _BF16 or t.get_device() != device:
         raise ValueError("%s must be a bf16 tensor on the queries' CUDA device" % name)
-    if len(tokens) == 2:
-        if len(shape) != 4 or shape[0] != tokens[0] or shape[3 - heads_at] != tokens[1]:
-            raise ValueError("%s must be a 4-D tensor of the queries' tokens" % name)
-        strides = (st[0], st[3 - heads_at], st[heads_at])
-    else:
-        if len(shape) != 3 or shape[0] != tokens[0]:
-            raise ValueError("%s must be a (total, heads, head_dim) tensor of the queries' tokens"
-                             % name)
-        strides = (0, st[0], st[1])
+    shape, st = t.shape, t.stride()
+    if len(shape) != len(tokens) + 2 or shape[0] != tokens[0] or (
+            len(shape) == 4 and shape[3 - heads_at] != tokens[1]):
+        raise ValueError("%s must have the queries' tokens" % name)
     if shape[-1] != d or st[-1] != 1:
         raise ValueError("%s must hold head_dim consecutive values per head" % name)
-    return fa_heads_t(t.data_ptr(), shape[heads_at], *strides)
+    if len(shape) == 4:
+        return fa_heads_t(t.data_ptr(), shape[heads_at], st[0], st[3 - heads_at], st[heads_at])
+    return fa_heads_t(t.data_ptr(), shape[1], 0, st[0], st[1])
 
 
 def _aux(t, name, dtype, device, shape):
-    """The address of a contiguous tensor of the given type and shape on `device` (0: None)."""
+    """The address of a contiguous tensor of the given type and shape on CUDA device number
+    `device`; None for None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor on the queries' device"
                          % (name, str(dtype).replace("torch.", "")))
     if t.shape != shape:
@@ -697,8 +698,8 @@ def qk_norm_rope_forward(q, k, v=None, q_weight=None, k_weight=None, eps=1e-6, n
             return qk_norm_rope_forward(q, k, v, q_weight, k_weight, eps, norm, inv_freq,
                                         positions, pair_axis, interleaved, seq_lengths,
                                         cu_seqlens, max_seqlen, stream)
-    tokens, d, device = tuple(q.shape[:-2]), q.shape[-1], q.device
-    at = len(tokens)
+    *tokens, _, d = q.shape
+    tokens, device, at = tuple(tokens), q.get_device(), len(tokens)
     ins = (_rows(q, "q", tokens, d, device, at), _rows(k, "k", tokens, d, device, at),
            _rows(v, "v", tokens, d, device, at))
     B, N, params = _norm_rope_params(device, tokens, d, q_weight, k_weight, eps, norm, inv_freq,
@@ -706,19 +707,19 @@ def qk_norm_rope_forward(q, k, v=None, q_weight=None, k_weight=None, eps=1e-6, n
                                      max_seqlen)
     res, outs = [], []
     for r in ins:
+        h = 0 if r is None else r.heads
         if r is None:
-            outs.append(None)
-            continue
-        h = r.heads
-        if at == 2:
+            t = out = None
+        elif at == 2:
             t = q.new_empty((B, h, N, d))
-            outs.append(fa_heads_t(t.data_ptr(), h, h * N * d, d, N * d))
+            out = fa_heads_t(t.data_ptr(), h, h * N * d, d, N * d)
         else:
             t = q.new_empty((tokens[0], h, d))
-            outs.append(fa_heads_t(t.data_ptr(), h, 0, h * d, d))
+            out = fa_heads_t(t.data_ptr(), h, 0, h * d, d)
         res.append(t)
+        outs.append(out)
     fa_qk_norm_rope_fwd(*ins, *outs, B, N, d, params, stream)
-    return tuple(res)
+    return tuple(res) if v is not None else tuple(res[:2])
 
 
 def qk_norm_rope_backward(dq, dk, dv=None, q=None, k=None, q_weight=None, k_weight=None, eps=1e-6,
@@ -742,7 +743,7 @@ def qk_norm_rope_backward(dq, dk, dv=None, q=None, k=None, q_weight=None, k_weig
         tokens = (dq.shape[0],)
     else:
         raise ValueError("dq must be (B, heads, N, d) or packed (total, heads, d)")
-    d, device, at = dq.shape[-1], dq.device, len(tokens)
+    d, device, at = dq.shape[-1], dq.get_device(), len(tokens)
     grads = [_rows(t, n, tokens, d, device, 1) for t, n in ((dq, "dq"), (dk, "dk"), (dv, "dv"))]
     if norm and (q is None or k is None):
         raise ValueError("the norm's gradient needs q and k")
@@ -767,6 +768,6 @@ def qk_norm_rope_backward(dq, dk, dv=None, q=None, k=None, q_weight=None, k_weig
     gkw = torch.empty_like(k_weight) if k_weight is not None else None
     ws = None
     if gqw is not None or gkw is not None:
-        ws = _scratch(fa_qk_norm_rope_workspace_bytes(d), device, stream)
+        ws = _scratch(fa_qk_norm_rope_workspace_bytes(d), dq.device, stream)
     fa_qk_norm_rope_bwd(*grads, xq, xk, *outs, gqw, gkw, B, N, d, params, ws, stream)
     return out[0], out[1], out[2], gqw, gkw

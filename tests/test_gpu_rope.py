@@ -241,10 +241,10 @@ def test_tiles_of_a_packed_batch(d, given):
     q, k, v = x.split(heads, -2)
     ref = fa.qk_norm_rope_forward(q, k, v, **kw, **call)
     y = x.clone()
-    B, N, params = fa._norm_rope_params(y.device, (total,), d, kw["q_weight"], kw["k_weight"],
+    B, N, params = fa._norm_rope_params(0, (total,), d, kw["q_weight"], kw["k_weight"],
                                         1e-6, True, kw["inv_freq"], kw.get("positions"), None,
                                         False, None, call["cu_seqlens"], N)
-    parts = [fa._rows(t, "x", (total,), d, y.device, 1) for t in y.split(heads, 1)]
+    parts = [fa._rows(t, "x", (total,), d, 0, 1) for t in y.split(heads, 1)]
     fa.fa_qk_norm_rope_fwd(*parts, *parts, B, N, d, params)
     for a, b in zip(y.split(heads, 1), ref):
         assert torch.equal(a.cpu()[torch.from_numpy(live)], b.cpu()[torch.from_numpy(live)])
@@ -373,10 +373,10 @@ def test_in_place():
     q, k, v = x.split((4, 2, 2), 1)
     ref = fa.qk_norm_rope_forward(q, k, v, **kw, **call)
     y = x.clone()
-    B, N, params = fa._norm_rope_params(y.device, (77,), 128, kw["q_weight"], kw["k_weight"],
+    B, N, params = fa._norm_rope_params(0, (77,), 128, kw["q_weight"], kw["k_weight"],
                                         1e-6, True, kw["inv_freq"], None, None, False, None, cu,
                                         64)
-    parts = [fa._rows(t, "x", (77,), 128, y.device, 1) for t in y.split((4, 2, 2), 1)]
+    parts = [fa._rows(t, "x", (77,), 128, 0, 1) for t in y.split((4, 2, 2), 1)]
     fa.fa_qk_norm_rope_fwd(*parts, *parts, B, N, 128, params)
     for a, b in zip(y.split((4, 2, 2), 1), ref):
         assert torch.equal(a, b)
