@@ -75,18 +75,22 @@ fa_status_t dispatch_features(std::integer_sequence<int, Fs...>, int feat, Args&
 
 // forward: every combination of ALiBi, key padding, residual and dropout, in the (B, H, N, d)
 // layout and packed (kFeatPacked = 32), each also with capped scores or a prefix
-// (kFeatScore = 64); at head_dim 128 also the e4m3 forward
+// (kFeatScore = 64), and without ALiBi also with a cap that needs no running maximum (kFeatScore |
+// kFeatNoMax = 192); at head_dim 128 also the e4m3 forward
 using FwdFeatures64 = std::integer_sequence<int, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14,
                                             15, 32, 33, 34, 35, 36, 37, 38, 39, 40, 41, 42, 43,
                                             44, 45, 46, 47, 64, 65, 66, 67, 68, 69, 70, 71, 72,
                                             73, 74, 75, 76, 77, 78, 79, 96, 97, 98, 99, 100, 101,
-                                            102, 103, 104, 105, 106, 107, 108, 109, 110, 111>;
+                                            102, 103, 104, 105, 106, 107, 108, 109, 110, 111,
+                                            192, 194, 196, 198, 200, 202, 204, 206, 224, 226,
+                                            228, 230, 232, 234, 236, 238>;
 using FwdFeatures128 = std::integer_sequence<int, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13,
                                              14, 15, 16, 32, 33, 34, 35, 36, 37, 38, 39, 40, 41,
                                              42, 43, 44, 45, 46, 47, 64, 65, 66, 67, 68, 69, 70,
                                              71, 72, 73, 74, 75, 76, 77, 78, 79, 96, 97, 98, 99,
                                              100, 101, 102, 103, 104, 105, 106, 107, 108, 109,
-                                             110, 111>;
+                                             110, 111, 192, 194, 196, 198, 200, 202, 204, 206,
+                                             224, 226, 228, 230, 232, 234, 236, 238>;
 // backward passes: ALiBi, key padding and dropout (the residual only changes delta), in both
 // layouts, with and without kFeatScore; the fused pass only in the (B, H, N, d) layout and
 // without kFeatScore
@@ -306,7 +310,7 @@ fa_status_t fused_pass(const void* q, const void* k, const void* v, const void* 
   const int right = fa::resolve_right(causal, window.right);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const Problem pb{B * H, H, N, scale, window.left, right};
-  const int feat = x.features() & ~fa::kFeatResidual;
+  const int feat = x.features() & ~(fa::kFeatResidual | fa::kFeatNoMax);
   const Extras xs = with_sched(x, workspace, B, H, N, d);
   s = dispatch_features<FusedLaunch>(FusedFeatures(), feat, q, k, v, dout, workspace,
                                      dq_acc_of(workspace, B, H, N), dk, dv, pb, xs, st);
@@ -341,7 +345,7 @@ fa_status_t dkdv_pass(const void* q, const void* k, const void* v, const void* d
   const int right = fa::resolve_right(causal, window.right);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int l = window.left, BH = B * H;
-  const int feat = x.features() & ~fa::kFeatResidual;
+  const int feat = x.features() & ~(fa::kFeatResidual | fa::kFeatNoMax);
   const Problem pb{BH, H, N, scale, l, right};
   const Extras xs = with_sched(x, workspace, B, H, N, d);
   s = d == 64 ? dispatch_features<DkdvLaunch<64>>(BwdFeatures(), feat, q, k, v, dout, workspace,
@@ -364,7 +368,7 @@ fa_status_t dq_pass(const void* q, const void* k, const void* v, const void* dou
   const int right = fa::resolve_right(causal, window.right);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int l = window.left, BH = B * H;
-  const int feat = x.features() & ~fa::kFeatResidual;
+  const int feat = x.features() & ~(fa::kFeatResidual | fa::kFeatNoMax);
   const Problem pb{BH, H, N, scale, l, right};
   const Extras xs = with_sched(x, workspace, B, H, N, d);
   s = d == 64 ? dispatch_features<DqLaunch<64>>(BwdFeatures(), feat, q, k, v, dout, workspace,

@@ -73,8 +73,9 @@ struct FwdArgs {
   CapArgs cap;               // kFeatScore: the cap of the scores
 };
 
-// kFp8: 8-bit (e4m3) Q, K, V tiles (head_dim 128 only: one 128-byte row per token).
-template <int D, bool kFp8 = false>
+// kFp8: 8-bit (e4m3) Q, K, V tiles (head_dim 128 only: one 128-byte row per token). kWide: two
+// warpgroups per stream, one for each half of a key tile (kFeatNoMax).
+template <int D, bool kFp8 = false, bool kWide = false>
 struct FwdCfg {
   static_assert(D == 64 || D == 128, "head_dim 64 or 128");
   static_assert(!kFp8 || D == 128, "the e4m3 forward is for head_dim 128");
@@ -111,9 +112,12 @@ struct FwdCfg {
   static constexpr int bPFull2 = bSFull2 + 2;        // + stream
   static constexpr int bODone2 = bPFull2 + 2;        // + stream
   static constexpr int bMmaFin = bODone2 + 2;        // + stream
-  static constexpr int kNumBars = bMmaFin + 2;
+  static constexpr int bSum = bMmaFin + 2;           // + stream (kWide): row sums exchanged
+  static constexpr int kNumBars = bMmaFin + (kWide ? 4 : 2);
   static constexpr int kMisc = kBar + kNumBars * 8;  // TMEM base address (+0), abort flag (+4)
-  static constexpr int kSmemBytes = kMisc + 16 + 1024;
+  static constexpr int kSums = kMisc + 16;           // kWide: the two row sums of each stream and half
+  static constexpr int kSched = kSums + (kWide ? 8 * kBlock * 4 : 0);  // varlen_item tables
+  static constexpr int kSmemBytes = kSched + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
   // tensor memory columns (128 lanes each)
   static constexpr uint32_t kTmemCols = 512;
@@ -129,9 +133,13 @@ struct FwdCfg {
   // on the other half.
   static constexpr bool kHalves = !kSepP;
   static constexpr uint32_t tP = 256 + 2 * D;  // + 64 * stream, when kSepP
-  static constexpr int kThreads = 352;  // 8 softmax warps, 2 MMA warps, producer warp
-  static constexpr int kWarpMma = 8;     // + stream
-  static constexpr int kWarpProducer = 10;
+  static constexpr int kSoftmaxWarps = kWide ? 16 : 8;
+  static constexpr int kWarpMma = kSoftmaxWarps;  // + stream
+  static constexpr int kWarpProducer = kSoftmaxWarps + 2;
+  static constexpr int kThreads = 32 * (kSoftmaxWarps + 3);
+  // warps that publish P (and free S) of a key tile: all of a stream's, at head_dim 128 those of
+  // a half
+  static constexpr int kPubWarps = kWide && kSepP ? 8 : 4;
 };
 
 // One work item: query tiles m[0] = 2p and m[1] = 2p + 1 (absent past the last tile) of
@@ -234,13 +242,15 @@ __device__ __forceinline__ FwdRange fwd_range(const FwdItem& it, int s) {
 // c tanh(s / c) as they are loaded (score.cuh; a.cap.on) and shows the first a.prefix[b] keys
 // to every query, both optional at run time.
 // 352 threads (11 warps, three of them on one SM sub-partition with its 16K registers): at
-// most 168 registers per thread.
+// most 168 registers per thread. kFeatNoMax: 608 threads, see the softmax warps.
 template <int D, int kFeat = 0>
-__global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 1)
+__global__ void __launch_bounds__(
+    FwdCfg<D, (kFeat & kFeatFp8) != 0, (kFeat & kFeatNoMax) != 0>::kThreads, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const FwdArgs a) {
   constexpr bool kFp8 = (kFeat & kFeatFp8) != 0;
-  using C = FwdCfg<D, kFp8>;
+  constexpr bool kWide = (kFeat & kFeatNoMax) != 0;
+  using C = FwdCfg<D, kFp8, kWide>;
   constexpr bool kAlibi = (kFeat & kFeatAlibi) != 0;
   constexpr bool kKpad = (kFeat & kFeatKpad) != 0;
   constexpr bool kResidual = (kFeat & kFeatResidual) != 0;
@@ -266,10 +276,11 @@ __global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 
       mbar_init(bar(C::bQFull + 2 * s + 1), 1);
       mbar_init(bar(C::bQEmpty + 2 * s + 1), 1);
       mbar_init(bar(C::bSFull + s), 1);
-      mbar_init(bar(C::bPFull + s), 4);
+      mbar_init(bar(C::bPFull + s), C::kPubWarps);
       mbar_init(bar(C::bODone + s), 1);
-      mbar_init(bar(C::bOFree + s), 4);
-      mbar_init(bar(C::bSFree + s), 4);
+      mbar_init(bar(C::bOFree + s), C::kSoftmaxWarps / 2);
+      mbar_init(bar(C::bSFree + s), C::kPubWarps);
+      if (kWide) mbar_init(bar(C::bSum + s), C::kSoftmaxWarps / 2);
       mbar_init(bar(C::bSFull2 + s), 1);
       mbar_init(bar(C::bPFull2 + s), 4);
       mbar_init(bar(C::bODone2 + s), 1);
@@ -292,7 +303,7 @@ __global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 
     tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
     tmem_relinquish();
   }
-  int* sched = reinterpret_cast<int*>(smem + C::kMisc + 16);
+  int* sched = reinterpret_cast<int*>(smem + C::kSched);
   if (a.sorted && warp == 1)
     build_varlen_sched(a.seq_len, cu, a.BH / a.H, a.H, a.N, a.per_item, a.n_pairs, sched);
   tc_fence_before();
@@ -586,6 +597,192 @@ __global__ void __launch_bounds__(FwdCfg<D, (kFeat & kFeatFp8) != 0>::kThreads, 
       mbar_wait(bar(C::bMmaFin + s), 0, nullptr);
     }
     __syncwarp();
+  } else if constexpr (kWide) {
+    // ------------------------------------------------- softmax warps without a running maximum
+    // The cap bounds every score, so P = 2^y is formed without the maximum of the row, and nothing
+    // is ever rescaled. Each warp then needs no other's scores: two warpgroups share a stream, one
+    // for the keys 0..63 of every tile and one for 64..127, twice the warps to hide each other's
+    // latencies (with one per stream the softmax warps' own instruction stream was the limit), each
+    // in a loop over 32 columns that keeps few registers and little code. They meet once per item,
+    // to add their row sums.
+    //   B32 H16 N2048 d64 causal, cap 50: 667 us (641 with one row sum) against 824 us with the
+    //   running maximum and 757 us without it in 8 warps (601 us without a cap); B2 H32 N4096 d128:
+    //   407 us against 425 us (350). With the two steps unrolled 2 to 5% slower: more code than the
+    //   instruction cache holds.
+    const int s = warp >> 3;                     // stream: query tile A or B of the item
+    const int h = (warp >> 2) & 1;               // half of the keys of a tile
+    const int r = threadIdx.x & 127;             // query row in the tile == TMEM lane
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + C::tS + 128u * s + 64u * h;
+    const uint32_t tP = C::kSepP ? tmem + lane_base + C::tP + 64u * s + 32u * h : tS;
+    const uint32_t tO = tmem + lane_base + C::tO + D * s + (D / 2) * h;
+    float* const sums = reinterpret_cast<float*>(smem + C::kSums) + 4 * kBlock * s;  // + 256 * half
+    int nt = 0;      // key tiles of this stream done (all items)
+    int nitems = 0;  // items of this stream done
+    bool ok = true;
+    for (int k = blockIdx.x; ok && k < a.n_items; k += gridDim.x) {
+      const FwdItem it = fwd_item<kPacked, kScore>(k, a, sched);
+      const FwdRange rg = fwd_range(it, s);
+      if (!rg.has) continue;
+      const Mask mk{it.n, a.left, a.right, it.prefix};
+      const int row = rg.m * kBlock + r;
+      // The sum of the weights as computed is for LSE. O is divided by the sum of the weights as
+      // they were rounded to bf16 for the product with V: without a maximum whose weight is exactly
+      // 1, that keeps O a mean of the rows of V (a row that sees one key returns it exactly), and
+      // rowsum(dO o O), from which the backward subtracts nearly equal numbers where one weight
+      // dominates, as accurate as the residual of O is meant to make it.
+      float l_run = 0.f, w_run = 0.f;
+      for (int j = rg.lo; j <= rg.hi; ++j) {
+        // keep flags of this row's 64 weights: bit c of keep[g] for key 64h + 32g + c
+        uint32_t keep[2] = {~0u, ~0u};
+        if (kDropout) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const uint32_t blk = (uint32_t)(8 * j + 4 * h + 2 * g);
+            keep[g] = keep_bits16(a.drop, blk, (uint32_t)row, (uint32_t)it.bh) |
+                      (keep_bits16(a.drop, blk + 1, (uint32_t)row, (uint32_t)it.bh) << 16);
+          }
+        }
+        const bool whole = tile_all_visible(rg.m, j, mk);
+        int c_lo = 0, c_hi = 63;
+        if (!whole) visible_keys(row, (long long)j * kBlock + 64 * h, 64, mk, c_lo, c_hi);
+        if (!mbar_wait_warp(bar((C::kHalves && h ? C::bSFull2 : C::bSFull) + s), nt & 1,
+                            abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        float2 lw = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          uint32_t u[32];
+          tmem_ld32(tS + 32 * q, u);
+          tmem_wait_ld();
+          reg_fence(u);
+          float y[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) y[c] = __uint_as_float(u[c]);
+          if (C::kSepP && q == 1) {
+            // this half of S_s is in registers: the next key tile's S_s may overwrite it
+            tc_fence_before();
+            mbar_arrive_warp(bar(C::bSFree + s));
+          }
+          cap_log2(y, a.cap);
+          if (!whole) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              y[c] = (c >= c_lo - 32 * q && c <= c_hi - 32 * q) ? y[c] : -INFINITY;
+          }
+          if (kKpad) {
+            const int col = j * kBlock + 64 * h + 32 * q + lane;
+            const uint32_t pm = __ballot_sync(
+                0xffffffffu, col < a.N && a.kpad[(size_t)(it.bh / a.H) * a.N + col] != 0);
+            if (pm != 0u) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) y[c] = ((pm >> c) & 1u) ? -INFINITY : y[c];
+            }
+          }
+          // with separate P, P_s is free once the previous P V has completed
+          if (C::kSepP && q == 0 && nt > 0) {
+            if (!mbar_wait_warp(bar(C::bODone + s), (nt - 1) & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+          }
+          const uint32_t kp = q == 0 ? keep[0] : keep[1];
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float p0 = ex2(y[2 * c]);
+            const float p1 = ex2(y[2 * c + 1]);
+            ls[c & 1] = __fadd2_rn(ls[c & 1], make_float2(p0, p1));
+            uint32_t w = pack_bf16x2(p0, p1);
+            lw = __fadd2_rn(lw, make_float2(__uint_as_float(w << 16),
+                                            __uint_as_float(w & 0xFFFF0000u)));
+            if (kDropout) {
+              w &= ((kp >> (2 * c)) & 1u ? 0xFFFFu : 0u) |
+                   ((kp >> (2 * c + 1)) & 1u ? 0xFFFF0000u : 0u);
+            }
+            pk[c] = w;
+          }
+          tmem_st16(tP + 16 * q, pk);
+        }
+        if (!ok) break;
+        l_run += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+        w_run += lw.x + lw.y;
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive_warp(bar((C::kHalves && h ? C::bPFull2 : C::bPFull) + s));
+        ++nt;
+      }
+      if (!ok) break;
+      // epilogue of the item, once its last P V product has completed: the two halves of each row's
+      // sum, then O / l (each warp its half of the columns) and LSE. (The partner has read the sums
+      // of the last item before it published its share of this one's last tile.)
+      if (!mbar_wait_warp(bar((C::kHalves ? C::bODone2 : C::bODone) + s), (nt - 1) & 1,
+                          abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      sums[2 * kBlock * h + r] = l_run;
+      sums[2 * kBlock * h + kBlock + r] = w_run;
+      mbar_arrive_warp(bar(C::bSum + s));
+      if (!mbar_wait_warp(bar(C::bSum + s), nitems & 1, abort_flag)) {
+        ok = false;
+        break;
+      }
+      ++nitems;
+      const float l = sums[r] + sums[2 * kBlock + r];
+      const float lr = sums[kBlock + r] + sums[3 * kBlock + r];
+      float inv_l = (lr > 0.f) ? 1.f / lr : 0.f;
+      if (kDropout) inv_l *= a.drop.keep_scale;
+      const int base = kPacked ? seq_base(cu, it.bh, a.H) : 0;
+      const bool written = kPacked ? row_written(cu, a.total, a.N, it.n, base, row) : row < a.N;
+      const size_t at =
+          row_at(cu, it.bh, a.H, a.N, base, written ? row : 0, D) + (size_t)(D / 2) * h;
+#pragma unroll
+      for (int q = 0; q < D / 64; ++q) {
+        uint32_t o[32];
+        tmem_ld32(tO + 32 * q, o);
+        tmem_wait_ld();
+        reg_fence(o);
+        uint32_t w[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          w[c] = pack_bf16x2(__uint_as_float(o[2 * c]) * inv_l, __uint_as_float(o[2 * c + 1]) * inv_l);
+        if (written) {
+#pragma unroll
+          for (int v4 = 0; v4 < 4; ++v4)
+            st_global_v4(a.o + at + 32 * q + 8 * v4, w[4 * v4], w[4 * v4 + 1], w[4 * v4 + 2],
+                         w[4 * v4 + 3]);
+        }
+        if (kResidual) {
+          // what rounding to bf16 left out, itself rounded to bf16
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float r0 = __uint_as_float(o[2 * c]) * inv_l - __uint_as_float(w[c] << 16);
+            const float r1 =
+                __uint_as_float(o[2 * c + 1]) * inv_l - __uint_as_float(w[c] & 0xFFFF0000u);
+            w[c] = pack_bf16x2(r0, r1);
+          }
+          if (written) {
+#pragma unroll
+            for (int v4 = 0; v4 < 4; ++v4)
+              st_global_v4(a.o_low + at + 32 * q + 8 * v4, w[4 * v4], w[4 * v4 + 1], w[4 * v4 + 2],
+                           w[4 * v4 + 3]);
+          }
+        }
+      }
+      // O_s has been read: the next item's first P V may overwrite it
+      tc_fence_before();
+      mbar_arrive_warp(bar(C::bOFree + s));
+      if (written && h == 0)
+        a.lse[lse_at(cu, a.total, it.bh, a.H, a.N, base, row)] =
+            (l > 0.f) ? log2f(l) * 0.69314718055994531f : -INFINITY;
+    }
   } else {
     // ------------------------------------------------------------------ softmax warps
     const int s = warp >> 2;                     // stream: query tile A or B of the item

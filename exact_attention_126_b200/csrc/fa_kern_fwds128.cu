@@ -11,6 +11,10 @@ FA_INSTANTIATE_FWD(128, 70) FA_INSTANTIATE_FWD(128, 71) FA_INSTANTIATE_FWD(128, 
 FA_INSTANTIATE_FWD(128, 73) FA_INSTANTIATE_FWD(128, 74) FA_INSTANTIATE_FWD(128, 75)
 FA_INSTANTIATE_FWD(128, 76) FA_INSTANTIATE_FWD(128, 77) FA_INSTANTIATE_FWD(128, 78)
 FA_INSTANTIATE_FWD(128, 79)
+// ... and without ALiBi with kFeatNoMax
+FA_INSTANTIATE_FWD(128, 192) FA_INSTANTIATE_FWD(128, 194) FA_INSTANTIATE_FWD(128, 196)
+FA_INSTANTIATE_FWD(128, 198) FA_INSTANTIATE_FWD(128, 200) FA_INSTANTIATE_FWD(128, 202)
+FA_INSTANTIATE_FWD(128, 204) FA_INSTANTIATE_FWD(128, 206)
 
 int take_status_fwds128() { return take_unit_status(); }
 

@@ -11,6 +11,10 @@ FA_INSTANTIATE_FWD(64, 70) FA_INSTANTIATE_FWD(64, 71) FA_INSTANTIATE_FWD(64, 72)
 FA_INSTANTIATE_FWD(64, 73) FA_INSTANTIATE_FWD(64, 74) FA_INSTANTIATE_FWD(64, 75)
 FA_INSTANTIATE_FWD(64, 76) FA_INSTANTIATE_FWD(64, 77) FA_INSTANTIATE_FWD(64, 78)
 FA_INSTANTIATE_FWD(64, 79)
+// ... and without ALiBi with kFeatNoMax
+FA_INSTANTIATE_FWD(64, 192) FA_INSTANTIATE_FWD(64, 194) FA_INSTANTIATE_FWD(64, 196)
+FA_INSTANTIATE_FWD(64, 198) FA_INSTANTIATE_FWD(64, 200) FA_INSTANTIATE_FWD(64, 202)
+FA_INSTANTIATE_FWD(64, 204) FA_INSTANTIATE_FWD(64, 206)
 
 int take_status_fwds64() { return take_unit_status(); }
 

@@ -11,6 +11,10 @@ FA_INSTANTIATE_FWD(128, 102) FA_INSTANTIATE_FWD(128, 103) FA_INSTANTIATE_FWD(128
 FA_INSTANTIATE_FWD(128, 105) FA_INSTANTIATE_FWD(128, 106) FA_INSTANTIATE_FWD(128, 107)
 FA_INSTANTIATE_FWD(128, 108) FA_INSTANTIATE_FWD(128, 109) FA_INSTANTIATE_FWD(128, 110)
 FA_INSTANTIATE_FWD(128, 111)
+// ... and without ALiBi with kFeatNoMax
+FA_INSTANTIATE_FWD(128, 224) FA_INSTANTIATE_FWD(128, 226) FA_INSTANTIATE_FWD(128, 228)
+FA_INSTANTIATE_FWD(128, 230) FA_INSTANTIATE_FWD(128, 232) FA_INSTANTIATE_FWD(128, 234)
+FA_INSTANTIATE_FWD(128, 236) FA_INSTANTIATE_FWD(128, 238)
 
 int take_status_fwdsp128() { return take_unit_status(); }
 

@@ -11,6 +11,10 @@ FA_INSTANTIATE_FWD(64, 102) FA_INSTANTIATE_FWD(64, 103) FA_INSTANTIATE_FWD(64, 1
 FA_INSTANTIATE_FWD(64, 105) FA_INSTANTIATE_FWD(64, 106) FA_INSTANTIATE_FWD(64, 107)
 FA_INSTANTIATE_FWD(64, 108) FA_INSTANTIATE_FWD(64, 109) FA_INSTANTIATE_FWD(64, 110)
 FA_INSTANTIATE_FWD(64, 111)
+// ... and without ALiBi with kFeatNoMax
+FA_INSTANTIATE_FWD(64, 224) FA_INSTANTIATE_FWD(64, 226) FA_INSTANTIATE_FWD(64, 228)
+FA_INSTANTIATE_FWD(64, 230) FA_INSTANTIATE_FWD(64, 232) FA_INSTANTIATE_FWD(64, 234)
+FA_INSTANTIATE_FWD(64, 236) FA_INSTANTIATE_FWD(64, 238)
 
 int take_status_fwdsp64() { return take_unit_status(); }
 

@@ -163,7 +163,7 @@ fa_status_t launch_fwd(const void* q, const void* k, const void* v, void* o, flo
              !map_rows(&mv, v, pb, x, D)) {
     return FA_ERR_CUDA;
   }
-  using C = fa::FwdCfg<D, kFp8>;
+  using C = fa::FwdCfg<D, kFp8, (kFeat & fa::kFeatNoMax) != 0>;
   fa::FwdArgs a;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;

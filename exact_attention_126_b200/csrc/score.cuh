@@ -28,6 +28,7 @@ struct CapArgs {
   float exp2u;       // 2 log2(e) scale / c
   float scale;       // scale / c
   float near[3];     // the short polynomial in (Q K^T)^2
+  float near2[3];    // ... times mul
 };
 
 // The arguments for a cap c of scores scaled by `scale`; c = 0: none.
@@ -46,6 +47,7 @@ inline CapArgs make_cap(float c, float scale) {
     r.near[i] = (float)(near[i] * p);
     p *= u * u;
   }
+  for (int i = 0; i < 3; ++i) r.near2[i] = r.near[i] * r.mul;
   r.scale = (float)u;
   return r;
 }
@@ -109,6 +111,19 @@ __device__ __forceinline__ void cap_tanh(float (&x)[N], const CapArgs& cap) {
     cap_poly<3>(x, cap.near);
   } else {
     cap_far(x, cap, m);
+  }
+}
+
+// x <- c log2(e) tanh(u).
+template <int N>
+__device__ __forceinline__ void cap_log2(float (&x)[N], const CapArgs& cap) {
+  const float m = cap_amax(x);
+  if (__builtin_expect(!__any_sync(0xffffffffu, m > cap.near_limit), 1)) {
+    cap_poly<3>(x, cap.near2);
+  } else {
+    cap_far(x, cap, m);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] *= cap.mul;
   }
 }
 

@@ -22,7 +22,14 @@ constexpr int kFeatDropout = 8;   // attention weights dropped with Philox keep 
 constexpr int kFeatFp8 = 16;      // forward on e4m3 Q, K, V (P in e4m3 for the P V product)
 constexpr int kFeatPacked = 32;   // a packed batch: (total, H, D) tensors, cumulative lengths
 constexpr int kFeatScore = 64;    // scores capped by a tanh and / or a prefix seen by all queries
+constexpr int kFeatNoMax = 128;   // forward, with kFeatScore: a cap that bounds the scores so far
+                                  // that the softmax needs no running maximum
 constexpr float kLog2e = 1.4426950408889634f;
+
+// The largest c log2(e) for which the softmax needs no running maximum: every capped score then
+// lies in [-80, 80] in log2 units, so that the weights 2^y, their sums and their products with V
+// stay far inside fp32's (and bf16's) exponents as they are.
+constexpr float kCapNoMax = 80.f;
 
 struct Mask {
   int N;      // sequence length

@@ -105,7 +105,7 @@ def test_cap(d, N, causal, window, cap):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("cap", [0.05, 0.5, 7.0, 300.0, 2000.0])
+@pytest.mark.parametrize("cap", [0.05, 0.5, 7.0, 55.0, 60.0, 300.0, 2000.0])
 def test_cap_sizes(d, cap):
     """From caps that hold every score to caps that hold none, rows on either side of the
     polynomial's range in one warp."""
@@ -128,6 +128,29 @@ def test_saturated_scores(d):
     assert rel_frob(out["o"].double().numpy(), o) < 5e-3
     assert np.abs(out["lse"].double().numpy() - lse).max() < 1e-3
     assert (out["dq"] == 0).all() and (out["dk"] == 0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap", [55.0, 56.0])
+def test_bounded_and_unbounded_maxima(d, cap):
+    """The forward keeps no running maximum up to a cap of 55 (c log2 e <= 80): rows whose scores
+    all lie at -c, all at +c, mixed and ordinary ones, with large and tiny values."""
+    g = torch.Generator().manual_seed(6)
+    B, H, N = 1, 2, 300
+    inp = inputs(B, H, N, d, 17)
+    inp["k"][..., 0] = 64.0
+    inp["q"][:, :, 0::4, 0] = -640.0   # every score at -c
+    inp["q"][:, :, 1::4, 0] = 640.0    # every score at +c
+    inp["k"][:, 1, ::2, 0] = -64.0     # the second head: half at either end
+    for big in (1e4, 1e-6):
+        inp["v"] = (big * torch.randn(B, H, N, d, generator=g)).to(BF16)
+        out = run(inp, 1.0 / d ** 0.5, False, softcap=cap)
+        f = {n: synth.to_f64(x) for n, x in inp.items()}
+        o, lse = oracle.fwd(f["q"], f["k"], f["v"], 1.0 / d ** 0.5, softcap=cap)
+        for r in range(4):
+            assert rel_frob(out["o"].double().numpy()[:, :, r::4], o[:, :, r::4]) < 5e-3
+        assert np.abs(out["lse"].double().numpy() - lse).max() < 1e-3
+        assert all(torch.isfinite(out[n]).all() for n in ("dq", "dk", "dv"))
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -161,9 +184,11 @@ def test_every_option_at_once(d, packed):
     g = torch.Generator().manual_seed(3)
     pad = torch.rand(B, N, generator=g) < 0.2
     pad[1] = True  # an entry without a visible key
-    check(inputs(B, H, N, d, 11, spread=2.0), 0.125, True, packed=packed, softcap=5.0,
-          prefixes=[100, 64, 0, 129], lengths=lens, alibi=[0.5, 0.1, 0.02], key_padding=pad,
-          dropout=(0.2, 1234, 5))
+    kw = dict(prefixes=[100, 64, 0, 129], lengths=lens, key_padding=pad, dropout=(0.2, 1234, 5))
+    inp = inputs(B, H, N, d, 11, spread=2.0)
+    check(inp, 0.125, True, packed=packed, softcap=5.0, alibi=[0.5, 0.1, 0.02], **kw)
+    check(inp, 0.125, True, packed=packed, softcap=5.0, **kw)
+    check(inp, 0.125, True, packed=packed, softcap=70.0, **kw)
 
 
 @pytest.mark.parametrize("d", [64, 128])
