@@ -69,6 +69,8 @@ struct FwdArgs {
   int sorted;                // variable-length batch: the schedule of varlen_item, whose
                              // tables each CTA builds in shared memory after kMisc
   float o_scale;             // kFeatFp8: the V descale, applied to O in the epilogue
+  int split;                 // kFeatNoMax with per_item = 1: stream B takes every second key tile
+                             // of the query tile instead of a query tile of its own
   const int* prefix;         // kFeatScore: B prefix lengths, or null
   CapArgs cap;               // kFeatScore: the cap of the scores
 };
@@ -156,6 +158,7 @@ struct FwdItem {
   int hi[2];
   int first;
   int last;
+  int step;     // key tiles from one that a stream sees to the next: 1, or 2 when it.split
 };
 
 __device__ __forceinline__ FwdItem no_fwd_item() {
@@ -169,12 +172,13 @@ __device__ __forceinline__ FwdItem no_fwd_item() {
   it.hi[0] = it.hi[1] = 0;
   it.first = 1;
   it.last = 0;
+  it.step = 1;
   return it;
 }
 
 // `sched`: the varlen_item tables (shared memory) when a.sorted; kPacked: a packed batch
-// (a.cu), else a.cu is not looked at; kScore: a.prefix likewise.
-template <bool kPacked, bool kScore>
+// (a.cu), else a.cu is not looked at; kScore: a.prefix likewise; kWide: a.split.
+template <bool kPacked, bool kScore, bool kWide>
 __device__ __forceinline__ FwdItem fwd_item(int k, const FwdArgs& a, const int* sched) {
   const int* const cu = kPacked ? a.cu : nullptr;
   FwdItem it;
@@ -200,14 +204,25 @@ __device__ __forceinline__ FwdItem fwd_item(int k, const FwdArgs& a, const int* 
   it.has_a = it.m[0] < n_qtiles;
   it.has_b = a.per_item == 2 && it.m[1] < n_qtiles;
   kv_tiles_for_q_tile(it.m[0], mk, it.lo[0], it.hi[0]);
+  it.step = 1;
+  it.first = it.lo[0];
+  it.last = it.hi[0];
+  if (kWide && a.split) {
+    // the key tiles in turn: lo, lo + 2, ... to stream A, lo + 1, lo + 3, ... to stream B
+    it.step = 2;
+    it.m[1] = it.m[0];
+    it.has_b = it.has_a && it.last > it.first;
+    it.lo[1] = it.first + 1;
+    it.hi[0] = it.last - ((it.last - it.first) & 1);
+    it.hi[1] = it.last - (((it.last - it.first) & 1) ^ 1);
+    return it;
+  }
   if (it.has_b) {
     kv_tiles_for_q_tile(it.m[1], mk, it.lo[1], it.hi[1]);
   } else {
     it.lo[1] = 1;
     it.hi[1] = 0;
   }
-  it.first = it.lo[0];
-  it.last = it.hi[0];
   if (it.has_b) {
     if (it.lo[1] < it.first) it.first = it.lo[1];
     if (it.hi[1] > it.last) it.last = it.hi[1];
@@ -221,6 +236,12 @@ struct FwdRange {
   int m;
   int lo;
   int hi;
+  int step;
+
+  // whether the stream sees key tile j
+  __device__ __forceinline__ bool sees(int j) const {
+    return has && lo <= j && j <= hi && (step == 1 || ((j - lo) & 1) == 0);
+  }
 };
 
 __device__ __forceinline__ FwdRange fwd_range(const FwdItem& it, int s) {
@@ -229,6 +250,7 @@ __device__ __forceinline__ FwdRange fwd_range(const FwdItem& it, int s) {
   r.m = s ? it.m[1] : it.m[0];
   r.lo = s ? it.lo[1] : it.lo[0];
   r.hi = s ? it.hi[1] : it.hi[0];
+  r.step = it.step;
   return r;
 }
 
@@ -321,7 +343,7 @@ __global__ void __launch_bounds__(
       int kc = 0, vc = 0;  // K and V loads issued (ring positions)
       bool ok = true;
       for (int k = blockIdx.x; ok && k < a.n_items; k += gridDim.x) {
-        const FwdItem it = fwd_item<kPacked, kScore>(k, a, sched);
+        const FwdItem it = fwd_item<kPacked, kScore, kWide>(k, a, sched);
         if (!it.has_a) continue;  // past the real length: nothing to load
         const int base = seq_base(cu, it.bh, a.H);
         for (int s = 0; s < 2; ++s) {
@@ -408,7 +430,7 @@ __global__ void __launch_bounds__(
       };
       // K step of key tile j (ring position p): S_s = Q_s K_j^T if the stream sees j
       auto k_step = [&](const FwdItem& it, const FwdRange& rg, int j, int p) -> bool {
-        const bool sees = rg.has && rg.lo <= j && j <= rg.hi;
+        const bool sees = rg.sees(j);
         const bool first = j == rg.lo;
         const int sk = p % C::kStagesK;
         if (!mbar_wait(bar(C::bKFull + sk), (p / C::kStagesK) & 1, abort_flag)) return false;
@@ -452,7 +474,7 @@ __global__ void __launch_bounds__(
       };
       // V step of key tile j (ring position p): O_s += P_s V_j if the stream sees j
       auto v_step = [&](const FwdItem& it, const FwdRange& rg, int j, int p) -> bool {
-        const bool sees = rg.has && rg.lo <= j && j <= rg.hi;
+        const bool sees = rg.sees(j);
         const bool first = j == rg.lo;
         const int sv = p % C::kStagesV;
         if (!mbar_wait(bar(C::bVFull + sv), (p / C::kStagesV) & 1, abort_flag)) return false;
@@ -497,7 +519,7 @@ __global__ void __launch_bounds__(
         const int sk = p % C::kStagesK;
         if (h == 0 && !mbar_wait(bar(C::bKFull + sk), (p / C::kStagesK) & 1, abort_flag))
           return false;
-        if (!(rg.has && rg.lo <= j && j <= rg.hi)) return true;
+        if (!rg.sees(j)) return true;
         const bool first = j == rg.lo;
         const int qb = 2 * s + nq % C::kQBufs;
         // S_h overwrites P_h of the previous key tile, whose P V must have completed
@@ -536,7 +558,7 @@ __global__ void __launch_bounds__(
         const int sv = p % C::kStagesV;
         if (h == 0 && !mbar_wait(bar(C::bVFull + sv), (p / C::kStagesV) & 1, abort_flag))
           return false;
-        if (rg.has && rg.lo <= j && j <= rg.hi) {
+        if (rg.sees(j)) {
           const bool first = j == rg.lo;
           // the item's first product overwrites O_s: the previous epilogue must have read it
           if (!mbar_wait(bar((h ? C::bPFull2 : C::bPFull) + s), nph[h] & 1, abort_flag) ||
@@ -567,15 +589,18 @@ __global__ void __launch_bounds__(
       };
 
       for (int k = blockIdx.x; ok && k < a.n_items; k += gridDim.x) {
-        const FwdItem it = fwd_item<kPacked, kScore>(k, a, sched);
+        const FwdItem it = fwd_item<kPacked, kScore, kWide>(k, a, sched);
         if (!it.has_a) continue;  // past the real length: no products
         const FwdRange rg = fwd_range(it, s);
         const int n = it.last - it.first + 1;
         if (C::kSepP) {
-          // S one key tile ahead of P V: S_s(j+1) is computed while the softmax works on j
+          // S one of the stream's key tiles ahead of P V: S_s(j+1) is computed while the softmax
+          // works on j
+          static_assert(!kWide || !C::kSepP || C::kStagesK >= 4, "K two tiles ahead of V");
           ok = k_step(it, rg, it.first, pos);
+          if (kWide && it.step == 2 && ok && n > 1) ok = k_step(it, rg, it.first + 1, pos + 1);
           for (int t = 0; ok && t < n; ++t) {
-            if (t + 1 < n) ok = k_step(it, rg, it.first + t + 1, pos + t + 1);
+            if (t + it.step < n) ok = k_step(it, rg, it.first + t + it.step, pos + t + it.step);
             if (ok) ok = v_step(it, rg, it.first + t, pos + t);
           }
         } else {
@@ -604,7 +629,8 @@ __global__ void __launch_bounds__(
     // for the keys 0..63 of every tile and one for 64..127, twice the warps to hide each other's
     // latencies (with one per stream the softmax warps' own instruction stream was the limit), each
     // in a loop over 32 columns that keeps few registers and little code. They meet once per item,
-    // to add their row sums.
+    // to add their row sums. And where query tiles are too few for two per SM, the two streams take
+    // a query tile's key tiles in turn (a.split): sums and products just add up.
     //   B32 H16 N2048 d64 causal, cap 50: 667 us (641 with one row sum) against 824 us with the
     //   running maximum and 757 us without it in 8 warps (601 us without a cap); B2 H32 N4096 d128:
     //   407 us against 425 us (350). With the two steps unrolled 2 to 5% slower: more code than the
@@ -619,9 +645,10 @@ __global__ void __launch_bounds__(
     float* const sums = reinterpret_cast<float*>(smem + C::kSums) + 4 * kBlock * s;  // + 256 * half
     int nt = 0;      // key tiles of this stream done (all items)
     int nitems = 0;  // items of this stream done
+    int npartner = 0;  // a.split, stream A: items that stream B shared
     bool ok = true;
     for (int k = blockIdx.x; ok && k < a.n_items; k += gridDim.x) {
-      const FwdItem it = fwd_item<kPacked, kScore>(k, a, sched);
+      const FwdItem it = fwd_item<kPacked, kScore, kWide>(k, a, sched);
       const FwdRange rg = fwd_range(it, s);
       if (!rg.has) continue;
       const Mask mk{it.n, a.left, a.right, it.prefix};
@@ -632,7 +659,7 @@ __global__ void __launch_bounds__(
       // rowsum(dO o O), from which the backward subtracts nearly equal numbers where one weight
       // dominates, as accurate as the residual of O is meant to make it.
       float l_run = 0.f, w_run = 0.f;
-      for (int j = rg.lo; j <= rg.hi; ++j) {
+      for (int j = rg.lo; j <= rg.hi; j += rg.step) {
         // keep flags of this row's 64 weights: bit c of keep[g] for key 64h + 32g + c
         uint32_t keep[2] = {~0u, ~0u};
         if (kDropout) {
@@ -729,14 +756,25 @@ __global__ void __launch_bounds__(
       tc_fence_after();
       sums[2 * kBlock * h + r] = l_run;
       sums[2 * kBlock * h + kBlock + r] = w_run;
+      tc_fence_before();
       mbar_arrive_warp(bar(C::bSum + s));
-      if (!mbar_wait_warp(bar(C::bSum + s), nitems & 1, abort_flag)) {
+      // a shared query tile is written by stream A's warps, which then also free O_B
+      if (it.step == 2 && s == 1) continue;
+      const bool shared = it.step == 2 && it.has_b;
+      if (!mbar_wait_warp(bar(C::bSum + s), nitems & 1, abort_flag) ||
+          (shared && !mbar_wait_warp(bar(C::bSum + 1), npartner & 1, abort_flag))) {
         ok = false;
         break;
       }
+      tc_fence_after();
       ++nitems;
-      const float l = sums[r] + sums[2 * kBlock + r];
-      const float lr = sums[kBlock + r] + sums[3 * kBlock + r];
+      if (shared) ++npartner;
+      float l = sums[r] + sums[2 * kBlock + r];
+      float lr = sums[kBlock + r] + sums[3 * kBlock + r];
+      if (shared) {
+        l += sums[4 * kBlock + r] + sums[6 * kBlock + r];
+        lr += sums[5 * kBlock + r] + sums[7 * kBlock + r];
+      }
       float inv_l = (lr > 0.f) ? 1.f / lr : 0.f;
       if (kDropout) inv_l *= a.drop.keep_scale;
       const int base = kPacked ? seq_base(cu, it.bh, a.H) : 0;
@@ -749,6 +787,15 @@ __global__ void __launch_bounds__(
         tmem_ld32(tO + 32 * q, o);
         tmem_wait_ld();
         reg_fence(o);
+        if (shared) {
+          uint32_t o2[32];
+          tmem_ld32(tO + D + 32 * q, o2);
+          tmem_wait_ld();
+          reg_fence(o2);
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            o[c] = __float_as_uint(__uint_as_float(o[c]) + __uint_as_float(o2[c]));
+        }
         uint32_t w[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c)
@@ -779,6 +826,7 @@ __global__ void __launch_bounds__(
       // O_s has been read: the next item's first P V may overwrite it
       tc_fence_before();
       mbar_arrive_warp(bar(C::bOFree + s));
+      if (shared) mbar_arrive_warp(bar(C::bOFree + 1));
       if (written && h == 0)
         a.lse[lse_at(cu, a.total, it.bh, a.H, a.N, base, row)] =
             (l > 0.f) ? log2f(l) * 0.69314718055994531f : -INFINITY;
@@ -801,7 +849,7 @@ __global__ void __launch_bounds__(
 
 
     for (int k = blockIdx.x; ok && k < a.n_items; k += gridDim.x) {
-      const FwdItem it = fwd_item<kPacked, kScore>(k, a, sched);
+      const FwdItem it = fwd_item<kPacked, kScore, kWide>(k, a, sched);
       const FwdRange rg = fwd_range(it, s);
       if (!rg.has) continue;
       const Mask mk{it.n, a.left, a.right, it.prefix};

@@ -219,6 +219,23 @@ def test_many_items_per_sm(d):
                                  (N, b, h))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N,lens", [(129, None), (1000, None), (700, [700, 0, 1, 128, 129, 300])])
+@pytest.mark.parametrize("packed", [False, True])
+def test_key_tiles_shared_by_two_streams(d, N, lens, packed):
+    """Few query tiles: a query tile's key tiles go to the block's two streams in turn, an odd and
+    an even number of them, one tile, and items of one and of several tiles on one SM."""
+    B = 6 if lens else 2
+    if packed and not lens:
+        lens = [N] * B
+    kw = dict(softcap=12.0, lengths=lens)
+    inp = inputs(B, 3, N, d, 31, spread=2.0)
+    pre = [(5 * N) // 7 if b % 2 else 3 for b in range(B)]
+    check(inp, 0.125, True, packed=packed, prefixes=pre, **kw)
+    check(inp, 0.125, False, packed=packed, **kw)
+    check(inp, 0.125, False, (150, 60), packed=packed, **kw)
+
+
 def test_no_cap_and_no_prefix_is_the_plain_call():
     dev = torch.device("cuda:0")
     inp = inputs(2, 2, 200, 64)
