@@ -1028,11 +1028,12 @@ __global__ void __launch_bounds__(
         }
         tc_fence_after();
         float mx = -INFINITY;
-        if constexpr (kScore) {
-          // Everything that changes the scores, and their maximum, in a loop over 32 columns that
-          // takes S from tensor memory and puts it back: with the 128 columns unrolled, as the
-          // kernels without kFeatScore have them, the loop body outgrew the instruction cache
-          // (the top stall; B32 H16 N2048 causal with a cap: 958 us unrolled, 855 us as a loop)
+        const bool rolled = kScore && a.cap.on;
+        if (rolled) {
+          // With a cap, everything that changes the scores, and their maximum, in a loop over 32
+          // columns that takes S from tensor memory and puts it back: with the 128 columns
+          // unrolled, as below, the loop body outgrew the instruction cache (the top stall; B32 H16
+          // N2048 causal with a cap: 958 us unrolled, 855 us as a loop)
           const bool whole = tile_all_visible(rg.m, j, mk);
           int c_lo = 0, c_hi = kBlock - 1;
           if (!whole) visible_keys(row, (long long)j * kBlock, kBlock, mk, c_lo, c_hi);
@@ -1097,7 +1098,7 @@ __global__ void __launch_bounds__(
           tc_fence_before();
           mbar_arrive_warp(bar(C::bSFree + s));
         }
-        if (kAlibi && !kScore) {
+        if (kAlibi && !rolled) {
           // key minus query index at column 0 of the tile
           const long long kq = (long long)j * kBlock - row;
           const float base = (float)kq;
@@ -1116,13 +1117,13 @@ __global__ void __launch_bounds__(
               x[c] = fmaf(x[c], sl2, -slope2 * fabsf(base + (float)c));
           }
         }
-        if (!kScore && !tile_all_visible(rg.m, j, mk)) {
+        if (!rolled && !tile_all_visible(rg.m, j, mk)) {
           int c_lo, c_hi;
           visible_keys(row, (long long)j * kBlock, kBlock, mk, c_lo, c_hi);
 #pragma unroll
           for (int c = 0; c < kBlock; ++c) x[c] = (c >= c_lo && c <= c_hi) ? x[c] : -INFINITY;
         }
-        if (kKpad && !kScore) {
+        if (kKpad && !rolled) {
           // padded keys of this tile: lane l reads the flag of key 32g + l, one ballot per
           // 32 keys; the same 128 bits for every row
           uint32_t pm[4];
@@ -1138,7 +1139,7 @@ __global__ void __launch_bounds__(
               x[c] = ((pm[c >> 5] >> (c & 31)) & 1u) ? -INFINITY : x[c];
           }
         }
-        if constexpr (!kScore) {
+        if (!rolled) {
           // 16 partial maxima: x[0..47], then two columns at a time up to x[111], then x[112..127]
           float t[16];
 #pragma unroll

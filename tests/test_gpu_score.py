@@ -236,6 +236,24 @@ def test_key_tiles_shared_by_two_streams(d, N, lens, packed):
     check(inp, 0.125, False, (150, 60), packed=packed, **kw)
 
 
+@pytest.mark.parametrize("N", [256, 5000])
+def test_timeout_is_reported(N):
+    """The capped kernels' waits are bounded too (the hook skips every V tile): two streams on one
+    query tile, and on one each."""
+    dev = torch.device("cuda:0")
+    q = torch.randn(1, 4 if N > 256 else 1, N, 64, device=dev).to(BF16)
+    fa.fa_debug_set_fault(1)
+    try:
+        fa.attention_forward(q, q, q, 0.125, True, softcap=5.0)
+        status = fa.fa_debug_status()
+    finally:
+        fa.fa_debug_set_fault(0)
+    assert status == 6 and fa.fa_debug_status() == 0
+    a = fa.attention_forward(q, q, q, 0.125, True, softcap=5.0)
+    b = fa.attention_forward(q, q, q, 0.125, True, softcap=5.0)
+    assert fa.fa_debug_status() == 0 and all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 def test_no_cap_and_no_prefix_is_the_plain_call():
     dev = torch.device("cuda:0")
     inp = inputs(2, 2, 200, 64)
