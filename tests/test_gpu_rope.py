@@ -355,6 +355,54 @@ def test_views_of_any_stride():
     assert (hold[mask] == 3.0).all()
 
 
+@pytest.mark.parametrize("N", [7, 6000])
+def test_rows_far_apart(N):
+    """Batch entries more than 2^31 elements from each other (views of a large buffer), through the
+    row kernels and through tiles."""
+    dev = torch.device("cuda:0")
+    heads, d, step = (8, 8, 8), 64, 3 << 30
+    x, kw = make((2, N), heads, d, d, 1)
+    hold = torch.empty(step + N * 24 * d, dtype=BF16, device=dev)
+    far = hold.as_strided((2, N, 24, d), (step, 24 * d, d, 1))
+    far.copy_(x)
+    ref = fa.qk_norm_rope_forward(*x.split(heads, 2), **kw)
+    got = fa.qk_norm_rope_forward(*far.split(heads, 2), **kw)
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    dy = [torch.randn_like(t) for t in ref]
+    q, k, v = x.split(heads, 2)
+    ref = fa.qk_norm_rope_backward(*dy, q=q, k=k, **kw)
+    q, k, v = far.split(heads, 2)
+    got = fa.qk_norm_rope_backward(*dy, q=q, k=k, out=far.split(heads, 2), **kw)  # in place
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+def test_calls_follow_their_tensors_device(monkeypatch):
+    """A call on tensors of another device than the current one runs there (here: the one device,
+    with the check made to say so once)."""
+    x, kw = make((2, 9), (2, 2, 2), 64, 64, 1)
+    q, k, v = x.split(2, 2)
+    ref = fa.qk_norm_rope_forward(q, k, v, **kw)
+    back = fa.qk_norm_rope_backward(*ref, q=q, k=k, **kw)
+    att = fa.attention_forward(*ref, causal=True, softcap=5.0)
+    grads = fa.attention_backward(*ref, *att, ref[0], causal=True, softcap=5.0)
+    entered = []
+
+    def elsewhere(t):
+        entered.append(t.device)
+        return len(entered) % 2 == 1  # the call itself; then the one under its device
+
+    monkeypatch.setattr(fa, "_elsewhere", elsewhere)
+    for f, args, kws, want in ((fa.qk_norm_rope_forward, (q, k, v), kw, ref),
+                               (fa.qk_norm_rope_backward, ref, dict(q=q, k=k, **kw), back),
+                               (fa.attention_forward, ref, dict(causal=True, softcap=5.0), att),
+                               (fa.attention_backward, ref + att + (ref[0],),
+                                dict(causal=True, softcap=5.0), grads)):
+        n = len(entered)
+        got = f(*args, **kws)
+        assert len(entered) == n + 2
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_shared_input_rows():
     """One key head read as several (stride 0)."""
     x, kw = make((2, 21), (4, 1, 1), 64, 64, 1)
