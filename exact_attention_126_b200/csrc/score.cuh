@@ -89,14 +89,32 @@ __device__ __forceinline__ float cap_exact(float x, const CapArgs& cap) {
 }
 
 // x <- tanh(u) where some score of the warp lies past the short polynomial's range (`m`: this
-// lane's largest magnitude).
-template <int N>
+// lane's largest magnitude). The exact form's error of 2e-7 in tanh is c log2(e) times that in the
+// exponent: past kCapCoarse (2^-12 in a weight, an eighth of P's rounding to bf16) scores that the
+// long polynomial covers keep it, whatever other scores their warp holds. kLarge: such caps occur.
+constexpr float kCapCoarse = 1024.f;
+
+template <bool kLarge, int N>
 __device__ __forceinline__ void cap_far(float (&x)[N], const CapArgs& cap, float m) {
+  const float a[5] = {0.999999893f, -0.333319542f, 0.133045259f, -0.0518218645f, 0.0150509423f};
   if (__any_sync(0xffffffffu, m > cap.limit)) {
+    if (kLarge && cap.mul > kCapCoarse) {
+      float y[N];  // (in local memory, for a loop: unrolled, the backward takes 1.5% longer)
+#pragma unroll
+      for (int i = 0; i < N; ++i) y[i] = x[i];
+#pragma unroll 1
+      for (int i = 0; i < N; ++i) {
+        const float u = y[i] * cap.scale, z = u * u;
+        const float p = u * fmaf(fmaf(fmaf(fmaf(a[4], z, a[3]), z, a[2]), z, a[1]), z, a[0]);
+        y[i] = fabsf(y[i]) > cap.limit ? cap_exact(y[i], cap) : p;
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = y[i];
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = cap_exact(x[i], cap);
   } else {
-    const float a[5] = {0.999999893f, -0.333319542f, 0.133045259f, -0.0518218645f, 0.0150509423f};
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] *= cap.scale;
     cap_poly<5>(x, a);
@@ -110,18 +128,18 @@ __device__ __forceinline__ void cap_tanh(float (&x)[N], const CapArgs& cap) {
   if (__builtin_expect(!__any_sync(0xffffffffu, m > cap.near_limit), 1)) {
     cap_poly<3>(x, cap.near);
   } else {
-    cap_far(x, cap, m);
+    cap_far<true>(x, cap, m);
   }
 }
 
-// x <- c log2(e) tanh(u).
+// x <- c log2(e) tanh(u), c log2(e) at most kCapNoMax.
 template <int N>
 __device__ __forceinline__ void cap_log2(float (&x)[N], const CapArgs& cap) {
   const float m = cap_amax(x);
   if (__builtin_expect(!__any_sync(0xffffffffu, m > cap.near_limit), 1)) {
     cap_poly<3>(x, cap.near2);
   } else {
-    cap_far(x, cap, m);
+    cap_far<false>(x, cap, m);
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] *= cap.mul;
   }
@@ -147,7 +165,7 @@ __device__ __forceinline__ void cap_tanh_tmem(float (&x)[N], const CapArgs& cap,
     float y[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(u[i]);
-    cap_far(y, cap, m);
+    cap_far<true>(y, cap, m);
 #pragma unroll
     for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(y[i]);
     tmem_st32(t + 32 * q, u);

@@ -216,7 +216,9 @@ fa_status_t fa_fwd_fp8(const void *q, const void *k, const void *v, float q_scal
  *            window (else FA_ERR_UNSUPPORTED).
  *   softcap  c > 0 caps the scaled scores s: they become c tanh(s / c), before an ALiBi bias, the
  *            mask and the softmax (LSE is that of the capped scores); 0 = no cap. c in
- *            [1e-30, 1e30] and scale / c in [1e-6, 1e6] (else FA_ERR_INVALID_ARG).
+ *            [1e-30, 1e30] and scale / c in [1e-6, 1e6] (else FA_ERR_INVALID_ARG). With a cap of
+ *            at most 55 and no bias, the fp32 sums behind O are of exp(score) V as it is, without
+ *            the row's maximum taken off: N max|V| must stay below 1e14, else O overflows.
  */
 typedef struct {
     const int *prefix_lengths;
@@ -415,7 +417,8 @@ fa_status_t fa_bwd_noalloc(const void *q, const void *k, const void *v, const vo
  * (strides in elements, multiples of 8 (FA_ERR_MISALIGNED), in [0, 2^40); a stride that is never
  * stepped is not looked at); data is 16-byte aligned. Rows that are read may overlap (stride 0:
  * shared rows); rows that are written must not (FA_ERR_INVALID_ARG), and may be the call's own
- * input rows, at the same address and strides. In a packed batch there is no batch dimension
+ * input rows of the same kind, at the same address and strides, if no other kind reads them (the
+ * data pointer of another kind, or other strides at the same one: FA_ERR_INVALID_ARG). In a packed batch there is no batch dimension
  * and token n is the n-th of the tensor. A null pointer or heads = 0 means none of that kind;
  * both sides of a call have the same heads of each kind (FA_ERR_INVALID_ARG). Heads need not be
  * the same for queries, keys and values. B N heads d (packed: total_tokens heads d) must be
