@@ -495,7 +495,9 @@ fa_status_t resolve_rows(const fa_heads_t* h, int B, int N, int d, bool packed, 
   *out = fa::HeadRows{nullptr, 0, 0, 0, 0};
   if (h == nullptr || h->heads == 0) return FA_OK;
   if (h->heads < 0 || h->data == nullptr) return FA_ERR_INVALID_ARG;
-  if ((packed ? (long long)N : (long long)B * N) * h->heads * d >= (1ll << 31))
+  // (fewer than 2^31 tokens: no product of these overflows)
+  if (h->heads >= (1 << 24) ||
+      (packed ? (long long)N : (long long)B * N) * h->heads * d >= (1ll << 31))
     return FA_ERR_UNSUPPORTED;
   // (stride, extent) of each dimension, the smallest stride first
   struct Dim {
@@ -574,6 +576,23 @@ fa_status_t resolve_rope(int B, int N, int d, const fa_norm_rope_t* p, fa::RopeA
   a->N = N;
   a->tokens = packed ? (B == 0 || N == 0 ? 0 : p->total_tokens) : B * N;
   return FA_OK;
+}
+
+// Whether rows are written where the call has those of another kind, or those of their own kind
+// at other strides.
+bool rows_collide(const fa::HeadRows (&written)[3], const fa::HeadRows (&other)[3],
+                  const fa::RopeArgs& a) {
+  for (int i = 0; i < 3; ++i) {
+    const fa::HeadRows& w = written[i];
+    for (int j = 0; j < 3; ++j) {
+      const fa::HeadRows& o = other[j];
+      if (w.heads == 0 || o.heads == 0 || w.data != o.data) continue;
+      if (i != j || (w.heads > 1 && w.sh != o.sh) || (a.tokens > 1 && a.N > 1 && w.sn != o.sn) ||
+          (a.cu == nullptr && a.B > 1 && w.sb != o.sb))
+        return true;
+    }
+  }
+  return false;
 }
 
 fa_status_t resolve_sides(const fa_heads_t* const (&in)[3], const fa_heads_t* const (&out)[3],
@@ -806,6 +825,7 @@ fa_status_t fa_qk_norm_rope_fwd(const fa_heads_t* q, const fa_heads_t* k, const 
   if ((s = resolve_sides({q, k, v}, {q_out, k_out, v_out}, true, d, a.cu != nullptr, a, a.x, a.y,
                          false, true)) != FA_OK)
     return s;
+  if (rows_collide(a.y, a.y, a) || rows_collide(a.y, a.x, a)) return FA_ERR_INVALID_ARG;
   if (a.y[0].heads + a.y[1].heads + a.y[2].heads == 0) return FA_OK;
   return fa_host::launch_rope_fwd(a, d, params->interleaved != 0,
                                   static_cast<cudaStream_t>(stream));
@@ -845,6 +865,8 @@ fa_status_t fa_qk_norm_rope_bwd(const fa_heads_t* dq, const fa_heads_t* dk, cons
                              false)) != FA_OK)
         return s;
     }
+    if (rows_collide(a.g, a.g, a) || rows_collide(a.g, a.y, a) || rows_collide(a.g, a.x, a))
+      return FA_ERR_INVALID_ARG;
   }
   if (a.y[0].heads + a.y[1].heads + a.y[2].heads == 0) a.tokens = 0;
   if (a.tokens == 0 && !gains) return FA_OK;

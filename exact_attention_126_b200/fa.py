@@ -508,7 +508,7 @@ def attention_forward(q, k, v, scale=None, causal=False, window=(-1, -1), stream
     wholly past it are not computed. cu_seqlens ((B + 1,) int32) with max_seqlen: a packed
     batch, q, k, v of shape (total, H, d) holding sequence b at tokens cu_seqlens[b] ..
     cu_seqlens[b+1]-1; O is (total, H, d) and LSE (H, total). softcap (c > 0): the scaled scores
-    s become c tanh(s / c). prefix_lengths ((B,) int32), for causal problems: query i of
+    s become c tanh(s / c) (with c up to 55, N max|V| must stay below 1e14). prefix_lengths ((B,) int32), for causal problems: query i of
     sequence b also sees every key j < prefix_lengths[b]."""
     if _elsewhere(q):
         with torch.cuda.device(q.device):
@@ -698,8 +698,10 @@ def qk_norm_rope_forward(q, k, v=None, q_weight=None, k_weight=None, eps=1e-6, n
             return qk_norm_rope_forward(q, k, v, q_weight, k_weight, eps, norm, inv_freq,
                                         positions, pair_axis, interleaved, seq_lengths,
                                         cu_seqlens, max_seqlen, stream)
-    *tokens, _, d = q.shape
-    tokens, device, at = tuple(tokens), q.get_device(), len(tokens)
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be (B, N, heads, d) or packed (total, heads, d)")
+    tokens, d, device = tuple(q.shape[:-2]), q.shape[-1], q.get_device()
+    at = len(tokens)
     ins = (_rows(q, "q", tokens, d, device, at), _rows(k, "k", tokens, d, device, at),
            _rows(v, "v", tokens, d, device, at))
     B, N, params = _norm_rope_params(device, tokens, d, q_weight, k_weight, eps, norm, inv_freq,

@@ -109,6 +109,30 @@ def test_backward_refusals(lib):
     assert bwd(d=32) == 2
 
 
+def test_written_rows_that_others_use(lib):
+    """Rows written at the data pointer of another kind, or of their own kind at other strides."""
+    r = [rows(data=A * (i + 1)) for i in range(6)]
+    p = ctypes.byref(params())
+    fwd = lambda *t: lib.fa_qk_norm_rope_fwd(*t, 2, 5, 64, p, None)  # noqa
+    assert fwd(r[0], r[1], r[2], r[3], r[3], r[5]) == 1
+    assert fwd(r[0], r[1], r[2], r[1], r[4], r[5]) == 1
+    assert fwd(r[0], r[1], r[2], r[3], r[4], r[0]) == 1
+    head_major = rows(data=A, token_stride=64, head_stride=5 * 64)
+    assert fwd(r[0], r[1], r[2], head_major, r[4], r[5]) == 1
+    bwd = lambda *t: lib.fa_qk_norm_rope_bwd(*t, None, None, 2, 5, 64, p, None, 0, None)  # noqa
+    g = [rows(data=A * (i + 7)) for i in range(3)]
+    assert bwd(r[0], r[1], r[2], r[3], r[4], g[0], g[0], g[2]) == 1
+    assert bwd(r[0], r[1], r[2], r[3], r[4], r[1], g[1], g[2]) == 1
+    assert bwd(r[0], r[1], r[2], r[3], r[4], g[0], g[1], r[3]) == 1
+    assert bwd(r[0], r[1], r[2], r[3], r[4], head_major, g[1], g[2]) == 1
+
+
+def test_heads_past_counting(lib):
+    """Counts of heads whose product with the tokens would not fit 64 bits."""
+    many = rows(heads=1 << 30, head_stride=0, token_stride=0, batch_stride=0)
+    assert fwd(lib, q=many, qo=many, B=1 << 15, N=1 << 15, d=128) == 2
+
+
 def test_struct_layouts(tmp_path):
     import shutil
     import subprocess
@@ -139,3 +163,13 @@ def test_binding_refuses_host_tensors():
         fa.qk_norm_rope_forward(q, q)
     with pytest.raises(ValueError):
         fa.qk_norm_rope_backward(q, q, q=q, k=q)
+
+
+def test_binding_refuses_rows_without_tokens(monkeypatch):
+    monkeypatch.setattr(fa, "_elsewhere", lambda t: False)
+    for shape in ((2, 64), (64,), (1, 1, 2, 3, 64)):
+        q = torch.zeros(shape, dtype=torch.bfloat16)
+        with pytest.raises(ValueError):
+            fa.qk_norm_rope_forward(q, q)
+        with pytest.raises(ValueError):
+            fa.qk_norm_rope_backward(q, q, norm=False)
