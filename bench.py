@@ -38,30 +38,31 @@ L2_BYTES = 126 * 1024 * 1024
 # workload, from one ncu capture, with the SHA-256 of the sources that kernel was built from
 # (kernel_source_hash(kernel)); an entry whose hash no longer matches is reported as null.
 MEASURED_TRAFFIC = {
-    ("c4_causal_b32h16n2048d64", "fwd"): (639792640, "0bb51163869f",
-                                          "ncu --set full, one launch"),
-    ("c5_causal_b2h32n8192d128", "fwd"): (647730944, "0bb51163869f",
-                                          "ncu --set full, one launch"),
-    ("c4_causal_varlen_b32h16n2048d64", "fwd"): (778232576, "0bb51163869f",
-                                                 "ncu --set full, one launch"),
-    ("c4_causal_packed_b32h16n2048d64", "fwd"): (748935168, "0bb51163869f",
-                                                 "ncu --set full, one launch"),
-    ("c4_causal_b32h16n2048d64", "bwd_preprocess"): (417532416, "7b14b8ee8bec",
-                                                     "ncu --set full, one launch"),
-    ("c4_causal_b32h16n2048d64", "bwd_dkdv"): (785412864, "7b14b8ee8bec",
-                                               "ncu --set full, one launch"),
-    ("c4_causal_b32h16n2048d64", "bwd_dq"): (665136384, "7b14b8ee8bec",
-                                             "ncu --set full, one launch"),
-    ("c5_causal_b2h32n8192d128", "bwd_dkdv"): (782708224, "7b14b8ee8bec",
-                                               "ncu --set full, one launch"),
-    ("c5_causal_b2h32n8192d128", "bwd_dq"): (665543424, "7b14b8ee8bec",
-                                             "ncu --set full, one launch"),
+    ("c4_causal_b32h16n2048d64", "fwd"): (634789632, "17b04ffd61e8",
+                                          "ncu DRAM counters, one launch"),
+    ("c5_causal_b2h32n8192d128", "fwd"): (643814400, "17b04ffd61e8",
+                                          "ncu DRAM counters, one launch"),
+    ("c4_causal_varlen_b32h16n2048d64", "fwd"): (784029696, "17b04ffd61e8",
+                                                 "ncu DRAM counters, one launch"),
+    ("c4_causal_packed_b32h16n2048d64", "fwd"): (754728448, "17b04ffd61e8",
+                                                 "ncu DRAM counters, one launch"),
+    ("c4_causal_b32h16n2048d64", "bwd_preprocess"): (413157888, "e0a6afe649e7",
+                                                     "ncu DRAM counters, one launch"),
+    ("c4_causal_b32h16n2048d64", "bwd_dkdv"): (780847104, "e0a6afe649e7",
+                                               "ncu DRAM counters, one launch"),
+    ("c4_causal_b32h16n2048d64", "bwd_dq"): (660481536, "e0a6afe649e7",
+                                             "ncu DRAM counters, one launch"),
+    ("c5_causal_b2h32n8192d128", "bwd_dkdv"): (779104512, "e0a6afe649e7",
+                                               "ncu DRAM counters, one launch"),
+    ("c5_causal_b2h32n8192d128", "bwd_dq"): (657946112, "e0a6afe649e7",
+                                             "ncu DRAM counters, one launch"),
 }
 
 
 # The sources each kernel is compiled from, besides the shared headers: a measured traffic
 # figure stays valid while these are unchanged.
-COMMON_SOURCES = ("sm100.cuh", "tiles.cuh", "rng.cuh", "launch_impl.cuh", "launch.h")
+COMMON_SOURCES = ("sm100.cuh", "tiles.cuh", "score.cuh", "rng.cuh", "launch_impl.cuh", "launch.h",
+                  "tma_maps.h")
 KERNEL_SOURCES = {
     "fwd": ("fa_fwd.cuh",),
     "bwd_preprocess": ("fa_bwd.cuh",),
