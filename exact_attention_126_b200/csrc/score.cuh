@@ -23,9 +23,8 @@ namespace fa {
 struct CapArgs {
   int on;            // 0: the scores are not capped
   float near_limit;  // |Q K^T| up to which the short polynomial holds: 0.25 c / scale
-  float limit;       // ... and the long one: 0.625 c / scale
+  float limit;       // ... and the long one: kCapLimit c / scale
   float mul;         // c log2(e): turns tanh(u) into log2 units
-  float exp2u;       // 2 log2(e) scale / c
   float scale;       // scale / c
   float near[3];     // the short polynomial in (Q K^T)^2
   float near2[3];    // ... times mul
@@ -40,7 +39,6 @@ inline CapArgs make_cap(float c, float scale) {
   r.near_limit = (float)(0.25 / u);
   r.limit = (float)(0.625 / u);
   r.mul = (float)(c * 1.4426950408889634);
-  r.exp2u = (float)(2.0 * 1.4426950408889634 * u);
   const double near[3] = {0.999999604, -0.333219082, 0.128416134};
   double p = u;
   for (int i = 0; i < 3; ++i) {
@@ -84,51 +82,59 @@ __device__ __forceinline__ void cap_poly(float (&x)[N], const float (&a)[K]) {
   }
 }
 
-__device__ __forceinline__ float cap_exact(float x, const CapArgs& cap) {
-  return fmaf(-2.f, rcp(ex2(x * cap.exp2u) + 1.f), 1.f);
+__device__ __forceinline__ float cap_exact(float u) {
+  return fmaf(-2.f, rcp(ex2(u * (2.f * kLog2e)) + 1.f), 1.f);
 }
 
-// x <- tanh(u) where some score of the warp lies past the short polynomial's range (`m`: this
-// lane's largest magnitude). The exact form's error of 2e-7 in tanh is c log2(e) times that in the
-// exponent: past kCapCoarse (2^-12 in a weight, an eighth of P's rounding to bf16) scores that the
-// long polynomial covers keep it, whatever other scores their warp holds. kLarge: such caps occur.
+// u <- tanh(u) where some score of the warp lies past the short polynomial's range; `exact`: past
+// the long one's. The exact form's error of 2e-7 in tanh is c log2(e) times that in the exponent:
+// past kCapCoarse (2^-12 in a weight, an eighth of P's rounding to bf16) scores that the long
+// polynomial covers keep it, whatever other scores their warp holds. kLarge: such caps occur.
+constexpr float kCapLimit = 0.625f;
 constexpr float kCapCoarse = 1024.f;
 
 template <bool kLarge, int N>
-__device__ __forceinline__ void cap_far(float (&x)[N], const CapArgs& cap, float m) {
+__device__ __forceinline__ void cap_far(float (&u)[N], const CapArgs& cap, bool exact) {
   const float a[5] = {0.999999893f, -0.333319542f, 0.133045259f, -0.0518218645f, 0.0150509423f};
-  if (__any_sync(0xffffffffu, m > cap.limit)) {
+  if (exact) {
     if (kLarge && cap.mul > kCapCoarse) {
       float y[N];  // (in local memory, for a loop: unrolled, the backward takes 1.5% longer)
 #pragma unroll
-      for (int i = 0; i < N; ++i) y[i] = x[i];
+      for (int i = 0; i < N; ++i) y[i] = u[i];
 #pragma unroll 1
       for (int i = 0; i < N; ++i) {
-        const float u = y[i] * cap.scale, z = u * u;
-        const float p = u * fmaf(fmaf(fmaf(fmaf(a[4], z, a[3]), z, a[2]), z, a[1]), z, a[0]);
-        y[i] = fabsf(y[i]) > cap.limit ? cap_exact(y[i], cap) : p;
+        const float x = y[i], z = x * x;
+        const float p = x * fmaf(fmaf(fmaf(fmaf(a[4], z, a[3]), z, a[2]), z, a[1]), z, a[0]);
+        y[i] = fabsf(x) > kCapLimit ? cap_exact(x) : p;
       }
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = y[i];
+      for (int i = 0; i < N; ++i) u[i] = y[i];
       return;
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = cap_exact(x[i], cap);
+    for (int i = 0; i < N; ++i) u[i] = cap_exact(u[i]);
   } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] *= cap.scale;
-    cap_poly<5>(x, a);
+    cap_poly<5>(u, a);
   }
+}
+
+// Its scores scaled first, their largest magnitude taken anew: kept from the check of the short
+// polynomial, it costs every tile a register, and the backward 3% (B32 H16 N2048 d64 causal, cap 50:
+// 1900 -> 1845 us).
+template <int N>
+__device__ __forceinline__ void cap_far(float (&x)[N], const CapArgs& cap) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] *= cap.scale;
+  cap_far<true>(x, cap, __any_sync(0xffffffffu, cap_amax(x) > kCapLimit) != 0);
 }
 
 // x <- tanh(u) of the N scores x of each lane of a warp.
 template <int N>
 __device__ __forceinline__ void cap_tanh(float (&x)[N], const CapArgs& cap) {
-  const float m = cap_amax(x);
-  if (__builtin_expect(!__any_sync(0xffffffffu, m > cap.near_limit), 1)) {
+  if (__builtin_expect(!__any_sync(0xffffffffu, cap_amax(x) > cap.near_limit), 1)) {
     cap_poly<3>(x, cap.near);
   } else {
-    cap_far<true>(x, cap, m);
+    cap_far(x, cap);
   }
 }
 
@@ -139,7 +145,11 @@ __device__ __forceinline__ void cap_log2(float (&x)[N], const CapArgs& cap) {
   if (__builtin_expect(!__any_sync(0xffffffffu, m > cap.near_limit), 1)) {
     cap_poly<3>(x, cap.near2);
   } else {
-    cap_far<false>(x, cap, m);
+    // (here the kept maximum is the faster: cap 20, 797 us against 820)
+    const bool exact = __any_sync(0xffffffffu, m > cap.limit) != 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] *= cap.scale;
+    cap_far<false>(x, cap, exact);
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] *= cap.mul;
   }
@@ -151,8 +161,7 @@ __device__ __forceinline__ void cap_log2(float (&x)[N], const CapArgs& cap) {
 // causal: 498 us unrolled, 449 us as a loop).
 template <int N>
 __device__ __forceinline__ void cap_tanh_tmem(float (&x)[N], const CapArgs& cap, uint32_t t) {
-  const float m = cap_amax(x);
-  if (__builtin_expect(!__any_sync(0xffffffffu, m > cap.near_limit), 1)) {
+  if (__builtin_expect(!__any_sync(0xffffffffu, cap_amax(x) > cap.near_limit), 1)) {
     cap_poly<3>(x, cap.near);
     return;
   }
@@ -165,7 +174,7 @@ __device__ __forceinline__ void cap_tanh_tmem(float (&x)[N], const CapArgs& cap,
     float y[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(u[i]);
-    cap_far<true>(y, cap, m);
+    cap_far(y, cap);
 #pragma unroll
     for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(y[i]);
     tmem_st32(t + 32 * q, u);
