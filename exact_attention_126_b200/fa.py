@@ -221,6 +221,10 @@ def attention_forward_fp8(q8, k8, v8, q_scale=1.0, k_scale=1.0, v_scale=1.0, sca
             raise ValueError("q8, k8, v8 must be float8_e4m3fn (or uint8) CUDA tensors")
         if not t.is_contiguous() or t.shape != q8.shape:
             raise ValueError("q8, k8, v8 must be contiguous and share one shape")
+    other = _other_stream(stream, q8.device)
+    if other is not None:
+        return _on_stream(other, attention_forward_fp8, q8, k8, v8, q_scale, k_scale, v_scale,
+                          scale, causal, window)
     B, H, N, d = _shape(q8)
     o = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=q8.device)
     lse = torch.empty((B, H, N), dtype=torch.float32, device=q8.device)
@@ -418,13 +422,35 @@ def _elsewhere(t):
     return t.get_device() != torch.cuda.current_device()
 
 
-def _scratch(nbytes, device, stream):
-    """A workspace that stays out of the allocator's hands until `stream` (None: the current
-    one) has passed the kernels launched on it."""
-    ws = torch.empty(max(1, nbytes), dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(torch.cuda.ExternalStream(_stream(stream), device=device))
-    return ws
+def _other_stream(stream, device):
+    """`stream` where it is not the current stream of `device` (the current device), else None."""
+    if stream is None or _stream(stream) == _stream(None):
+        return None
+    if not isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError("stream must be a stream of the tensors' device")
+    return stream
+
+
+def _on_stream(stream, call, *args):
+    """`call(*args)` with `stream` as the current stream: what the call allocates is then memory of
+    that stream, whose earlier users are ordered before the call's kernels (a block of the current
+    stream may still be in use there). The arguments stay out of the allocator's hands until
+    `stream`, the results until the caller's stream, has passed what is queued on it."""
+    home = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        res = call(*args)
+    for group, user in ((args, stream), (res, home)):
+        for x in group:
+            for t in x if isinstance(x, (list, tuple)) else (x,):
+                if isinstance(t, torch.Tensor):
+                    t.record_stream(user)
+    return res
+
+
+def _scratch(nbytes, device):
+    return torch.empty(max(1, nbytes), dtype=torch.uint8, device=device)
 
 
 def _check_inputs(*ts):
@@ -515,6 +541,11 @@ def attention_forward(q, k, v, scale=None, causal=False, window=(-1, -1), stream
             return attention_forward(q, k, v, scale, causal, window, stream, alibi_slopes,
                                      key_padding, keep_residual, dropout, seq_lengths, cu_seqlens,
                                      max_seqlen, softcap, prefix_lengths)
+    other = _other_stream(stream, q.device)
+    if other is not None:
+        return _on_stream(other, attention_forward, q, k, v, scale, causal, window, None,
+                          alibi_slopes, key_padding, keep_residual, dropout, seq_lengths,
+                          cu_seqlens, max_seqlen, softcap, prefix_lengths)
     _check_inputs(q, k, v)
     if cu_seqlens is not None:
         B, H, N, d = _packed_dims(q, cu_seqlens, max_seqlen, seq_lengths)
@@ -562,6 +593,11 @@ def attention_backward(q, k, v, o, lse, do, scale=None, causal=False, window=(-1
                                       alibi_slopes, key_padding, o_low, dropout, fused,
                                       seq_lengths, cu_seqlens, max_seqlen, softcap,
                                       prefix_lengths)
+    other = _other_stream(stream, q.device)
+    if other is not None:
+        return _on_stream(other, attention_backward, q, k, v, o, lse, do, scale, causal, window,
+                          None, alibi_slopes, key_padding, o_low, dropout, fused, seq_lengths,
+                          cu_seqlens, max_seqlen, softcap, prefix_lengths)
     _check_inputs(q, k, v, o, do)
     if cu_seqlens is not None:
         B, H, N, d = _packed_dims(q, cu_seqlens, max_seqlen, seq_lengths)
@@ -587,7 +623,7 @@ def attention_backward(q, k, v, o, lse, do, scale=None, causal=False, window=(-1
         opt = options(alibi_slopes, key_padding, o_low, *(dropout or ()),
                       fused=fused, seq_lengths=seq_lengths, cu_seqlens=cu_seqlens,
                       total_tokens=total)
-    ws = _scratch(fa_bwd_workspace_bytes_ex(B, H, N, d, opt), q.device, stream)
+    ws = _scratch(fa_bwd_workspace_bytes_ex(B, H, N, d, opt), q.device)
     if score is not None:
         fa_bwd_score(q, k, v, o, do, lse, dq, dk, dv, ws, opt, score, scale, causal, window,
                      stream, dims=(B, H, N, d))
@@ -698,6 +734,11 @@ def qk_norm_rope_forward(q, k, v=None, q_weight=None, k_weight=None, eps=1e-6, n
             return qk_norm_rope_forward(q, k, v, q_weight, k_weight, eps, norm, inv_freq,
                                         positions, pair_axis, interleaved, seq_lengths,
                                         cu_seqlens, max_seqlen, stream)
+    other = _other_stream(stream, q.device)
+    if other is not None:
+        return _on_stream(other, qk_norm_rope_forward, q, k, v, q_weight, k_weight, eps, norm,
+                          inv_freq, positions, pair_axis, interleaved, seq_lengths, cu_seqlens,
+                          max_seqlen)
     if q.dim() not in (3, 4):
         raise ValueError("q must be (B, N, heads, d) or packed (total, heads, d)")
     tokens, d, device = tuple(q.shape[:-2]), q.shape[-1], q.get_device()
@@ -739,6 +780,11 @@ def qk_norm_rope_backward(dq, dk, dv=None, q=None, k=None, q_weight=None, k_weig
             return qk_norm_rope_backward(dq, dk, dv, q, k, q_weight, k_weight, eps, norm,
                                          inv_freq, positions, pair_axis, interleaved, seq_lengths,
                                          cu_seqlens, max_seqlen, stream, out)
+    other = _other_stream(stream, dq.device)
+    if other is not None:
+        return _on_stream(other, qk_norm_rope_backward, dq, dk, dv, q, k, q_weight, k_weight, eps,
+                          norm, inv_freq, positions, pair_axis, interleaved, seq_lengths,
+                          cu_seqlens, max_seqlen, None, out)
     if dq.dim() == 4:
         tokens = (dq.shape[0], dq.shape[2])
     elif dq.dim() == 3:
@@ -770,6 +816,6 @@ def qk_norm_rope_backward(dq, dk, dv=None, q=None, k=None, q_weight=None, k_weig
     gkw = torch.empty_like(k_weight) if k_weight is not None else None
     ws = None
     if gqw is not None or gkw is not None:
-        ws = _scratch(fa_qk_norm_rope_workspace_bytes(d), dq.device, stream)
+        ws = _scratch(fa_qk_norm_rope_workspace_bytes(d), dq.device)
     fa_qk_norm_rope_bwd(*grads, xq, xk, *outs, gqw, gkw, B, N, d, params, ws, stream)
     return out[0], out[1], out[2], gqw, gkw
