@@ -579,15 +579,16 @@ fa_status_t resolve_rope(int B, int N, int d, const fa_norm_rope_t* p, fa::RopeA
 }
 
 // Whether rows are written where the call has those of another kind, or those of their own kind
-// at other strides.
+// at other strides. (A packed batch steps through all its tokens, however short its sequences.)
 bool rows_collide(const fa::HeadRows (&written)[3], const fa::HeadRows (&other)[3],
                   const fa::RopeArgs& a) {
+  const bool steps = (a.cu != nullptr ? a.tokens : a.N) > 1;
   for (int i = 0; i < 3; ++i) {
     const fa::HeadRows& w = written[i];
     for (int j = 0; j < 3; ++j) {
       const fa::HeadRows& o = other[j];
       if (w.heads == 0 || o.heads == 0 || w.data != o.data) continue;
-      if (i != j || (w.heads > 1 && w.sh != o.sh) || (a.tokens > 1 && a.N > 1 && w.sn != o.sn) ||
+      if (i != j || (w.heads > 1 && w.sh != o.sh) || (steps && w.sn != o.sn) ||
           (a.cu == nullptr && a.B > 1 && w.sb != o.sb))
         return true;
     }

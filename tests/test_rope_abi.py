@@ -127,6 +127,20 @@ def test_written_rows_that_others_use(lib):
     assert bwd(r[0], r[1], r[2], r[3], r[4], head_major, g[1], g[2]) == 1
 
 
+def test_packed_single_tokens_in_place_at_other_strides(lib):
+    """Sequences of one token each: the call steps through all of them by the token stride."""
+    p = ctypes.byref(params(cu_seqlens=A, total_tokens=5))
+    r = [rows(data=A * (i + 1)) for i in range(6)]
+    wide = rows(data=A, token_stride=2 * r[0].token_stride)
+    fwd = lambda *t: lib.fa_qk_norm_rope_fwd(*t, 5, 1, 64, p, None)  # noqa
+    assert fwd(r[0], r[1], r[2], wide, r[4], r[5]) == 1
+    assert fwd(wide, r[1], r[2], r[0], r[4], r[5]) == 1
+    bwd = lambda *t: lib.fa_qk_norm_rope_bwd(*t, None, None, 5, 1, 64, p, None, 0, None)  # noqa
+    g = [rows(data=A * (i + 7)) for i in range(3)]
+    assert bwd(r[0], r[1], r[2], r[3], r[4], wide, g[1], g[2]) == 1
+    assert bwd(r[3], r[1], r[2], r[0], r[4], wide, g[1], g[2]) == 1
+
+
 def test_heads_past_counting(lib):
     """Counts of heads whose product with the tokens would not fit 64 bits."""
     many = rows(heads=1 << 30, head_stride=0, token_stride=0, batch_stride=0)
