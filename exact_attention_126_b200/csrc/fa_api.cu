@@ -572,6 +572,7 @@ fa_status_t resolve_rope(int B, int N, int d, const fa_norm_rope_t* p, fa::RopeA
   a->w[1] = p->k_weight;
   a->seq_len = p->seq_lengths;
   a->cu = p->cu_seqlens;
+  a->fill = packed && p->fill_uncovered ? 1 : 0;
   a->B = B;
   a->N = N;
   a->tokens = packed ? (B == 0 || N == 0 ? 0 : p->total_tokens) : B * N;
@@ -917,7 +918,7 @@ fa_status_t fa_debug_set_fault(int fault) {
   return FA_OK;
 }
 
-int fa_version(void) { return 300; }
+int fa_version(void) { return 400; }
 
 }  // extern "C"
 #pragma GCC visibility pop

@@ -44,7 +44,7 @@ struct RopeToken {
   int n;       // row: n of entry b, or packed: the token's index
   int place;   // place in its sequence
   bool live;   // within its sequence's real length
-  bool owned;  // its rows are written (packed: some sequence covers it)
+  bool owned;  // its rows are written (packed: some sequence covers it, or a.fill)
 };
 
 __device__ __forceinline__ RopeToken rope_token(const RopeArgs& a, int t) {
@@ -71,7 +71,8 @@ __device__ __forceinline__ RopeToken rope_token(const RopeArgs& a, int t) {
   k.b = 0;
   k.n = t;
   k.place = t - start;
-  k.owned = k.live = t < a.tokens && lo < a.B && k.place >= 0 && k.place < a.N;
+  k.live = t < a.tokens && lo < a.B && k.place >= 0 && k.place < a.N;
+  k.owned = k.live || (a.fill && t < a.tokens);
   return k;
 }
 

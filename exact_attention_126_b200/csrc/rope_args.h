@@ -31,6 +31,7 @@ struct RopeArgs {
   const int* positions;     // (axes, tokens), or null (the place in the sequence)
   const int* seq_len;       // B real lengths of a padded batch, or null
   const int* cu;            // B + 1 cumulative lengths of a packed batch, or null
+  int fill;                 // packed: tokens that no sequence covers are written as zeros
   int B;
   int N;                    // rows per entry; packed: the longest sequence handled
   int tokens;               // B * N, or the packed tensors' tokens

@@ -74,7 +74,8 @@ class fa_norm_rope_t(ctypes.Structure):
                 ("positions", ctypes.c_void_p), ("seq_lengths", ctypes.c_void_p),
                 ("cu_seqlens", ctypes.c_void_p), ("eps", ctypes.c_float),
                 ("norm", ctypes.c_int), ("rotary_dim", ctypes.c_int), ("axes", ctypes.c_int),
-                ("interleaved", ctypes.c_int), ("total_tokens", ctypes.c_int)]
+                ("interleaved", ctypes.c_int), ("total_tokens", ctypes.c_int),
+                ("fill_uncovered", ctypes.c_int)]
 
 
 def options(alibi_slopes=None, key_padding=None, o_low=None, dropout_p=0.0, dropout_seed=0,
@@ -533,7 +534,8 @@ def attention_forward(q, k, v, scale=None, causal=False, window=(-1, -1), stream
     entry b holds seq_lengths[b] real tokens; rows past it are zero (LSE -inf) and tiles
     wholly past it are not computed. cu_seqlens ((B + 1,) int32) with max_seqlen: a packed
     batch, q, k, v of shape (total, H, d) holding sequence b at tokens cu_seqlens[b] ..
-    cu_seqlens[b+1]-1; O is (total, H, d) and LSE (H, total). softcap (c > 0): the scaled scores
+    cu_seqlens[b+1]-1; O is (total, H, d) and LSE (H, total), not written for tokens that no
+    sequence covers (nor are their gradients by attention_backward). softcap (c > 0): the scaled scores
     s become c tanh(s / c) (with c up to 55, N max|V| must stay below 1e14). prefix_lengths ((B,) int32), for causal problems: query i of
     sequence b also sees every key j < prefix_lengths[b]."""
     if _elsewhere(q):
@@ -728,7 +730,8 @@ def qk_norm_rope_forward(q, k, v=None, q_weight=None, k_weight=None, eps=1e-6, n
     (p, p + rotary_dim / 2), or (2p, 2p + 1) when interleaved, by position * inv_freq[p]; None =
     no rotation. positions ((B, N) or (total,) int32; None = the place in the sequence): with
     several axes (axes, B, N) or (axes, total), and pair_axis (rotary_dim / 2 uint8) names each
-    rotation's axis. seq_lengths ((B,) int32): rows past a length are zero."""
+    rotation's axis. seq_lengths ((B,) int32): rows past a length are zero, as are tokens of a
+    packed batch that no sequence covers (before the first, behind the last, past max_seqlen)."""
     if _elsewhere(q):
         with torch.cuda.device(q.device):
             return qk_norm_rope_forward(q, k, v, q_weight, k_weight, eps, norm, inv_freq,
@@ -761,6 +764,7 @@ def qk_norm_rope_forward(q, k, v=None, q_weight=None, k_weight=None, eps=1e-6, n
             out = fa_heads_t(t.data_ptr(), h, 0, h * d, d)
         res.append(t)
         outs.append(out)
+    params.fill_uncovered = 1  # (of memory that nothing has written yet)
     fa_qk_norm_rope_fwd(*ins, *outs, B, N, d, params, stream)
     return tuple(res) if v is not None else tuple(res[:2])
 
@@ -773,8 +777,9 @@ def qk_norm_rope_backward(dq, dk, dv=None, q=None, k=None, q_weight=None, k_weig
     (total, heads, d) (as attention_backward returns them): (gq, gk, gv, gq_weight, gk_weight),
     gv None without dv, the gains' None for a gain that is None. q, k: the forward's inputs
     (needed with norm). out: three tensors (the third None without dv) of the forward's input
-    shapes, of any strides that do not overlap, to write gq, gk, gv to; by default they are views
-    of one new (B, N, heads of all, d) or (total, heads of all, d) tensor."""
+    shapes, of any strides that do not overlap, to write gq, gk, gv to (tokens of a packed batch
+    that no sequence covers are left as they are there); by default they are views of one new
+    (B, N, heads of all, d) or (total, heads of all, d) tensor, zero for such tokens."""
     if _elsewhere(dq):
         with torch.cuda.device(dq.device):
             return qk_norm_rope_backward(dq, dk, dv, q, k, q_weight, k_weight, eps, norm,
@@ -805,6 +810,7 @@ def qk_norm_rope_backward(dq, dk, dv=None, q=None, k=None, q_weight=None, k_weig
         raise ValueError("q and k must have their gradients' heads")
     if out is None:
         out = list(dq.new_empty(tokens + (sum(heads), d)).split(heads, -2))
+        params.fill_uncovered = 1
     else:
         out = list(out) + [None] * (3 - len(out))
     if dv is None:

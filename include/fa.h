@@ -446,11 +446,13 @@ typedef struct {
  *   cu_seqlens, total_tokens
  *               a packed batch as in fa_options_t, or NULL / 0; offsets must not decrease. N is
  *               the longest sequence handled. Tokens that no sequence covers (before the first,
- *               behind the last, past N) are neither read nor written. Exclusive with
- *               seq_lengths (FA_ERR_INVALID_ARG).
+ *               behind the last, past N) do not enter the results and are not written, unless
+ *               fill_uncovered asks for it. Exclusive with seq_lengths (FA_ERR_INVALID_ARG).
  *   eps         finite, >= 0.
  *   rotary_dim  a multiple of 8 in [0, d] (else FA_ERR_UNSUPPORTED); 0: no rotation.
  *   axes        1 .. FA_MAX_AXES (above: FA_ERR_UNSUPPORTED); not looked at without rotation.
+ *   fill_uncovered  nonzero: tokens of a packed batch that no sequence covers are written as
+ *               zeros.
  */
 #define FA_MAX_AXES 3
 
@@ -468,6 +470,7 @@ typedef struct {
     int axes;
     int interleaved;
     int total_tokens;
+    int fill_uncovered;
 } fa_norm_rope_t;
 
 /* q_out, k_out, v_out from q, k, v (v and v_out may be NULL: queries and keys alone). */

@@ -325,6 +325,34 @@ def test_packed_batch(d, given):
         assert (f64(t)[~live] == 7.0).all() and not (f64(t)[live] == 7.0).all()
 
 
+@pytest.mark.parametrize("d,total", [(64, 170), (128, 170), (64, 19000), (128, 19000)])
+@pytest.mark.parametrize("norm", [True, False])
+def test_tokens_no_sequence_covers_are_zero(d, total, norm):
+    """In tensors that the call allocates: before the first sequence, behind the last, past N, and
+    where no sequence has a token at all; rows and tiles, on memory that held something else."""
+    N = total // 4
+    x, kw = make((total,), (6, 3, 5), d, d, 1, gains=norm)
+    x[:] = torch.randn_like(x)
+    q, k, v = x.split((6, 3, 5), 1)
+    for cu in ([3, 3 + N // 2, 3 + N // 2, 3 + 3 * N], [7, 7, 7, 7], [0, 1, 1, total - 1]):
+        live = np.zeros(total, bool)
+        for a, b in zip(cu[:-1], cu[1:]):
+            live[a:min(b, a + N)] = True
+        dead = torch.from_numpy(~live).to(x.device)
+        call = dict(cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=x.device), max_seqlen=N,
+                    norm=norm, **kw)
+        for _ in range(2):
+            junk = [torch.full_like(x, float("nan")), *(torch.full_like(t, float("nan"))
+                                                        for t in (q, k, v))]
+            torch.cuda.synchronize()
+            del junk
+            outs = fa.qk_norm_rope_forward(q, k, v, **call)
+            back = fa.qk_norm_rope_backward(*outs, q=q, k=k, **call)
+            for t in outs + back[:3]:
+                assert (t[dead] == 0).all() and torch.isfinite(t.float()).all()
+                assert (t[~dead].float().abs().amax((1, 2)) > 0).all()
+
+
 def test_views_of_any_stride():
     """A projection stored head-major, a slice of wider rows, one tensor of queries and keys, and
     gradients into strided outputs with sentinels around them."""
