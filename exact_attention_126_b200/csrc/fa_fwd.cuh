@@ -775,7 +775,8 @@ __global__ void __launch_bounds__(
         l += sums[4 * kBlock + r] + sums[6 * kBlock + r];
         lr += sums[5 * kBlock + r] + sums[7 * kBlock + r];
       }
-      float inv_l = (lr > 0.f) ? 1.f / lr : 0.f;
+      // (a sum of exactly 0 means no visible key; one that is not a number stays one)
+      float inv_l = (lr == 0.f) ? 0.f : 1.f / lr;
       if (kDropout) inv_l *= a.drop.keep_scale;
       const int base = kPacked ? seq_base(cu, it.bh, a.H) : 0;
       const bool written = kPacked ? row_written(cu, a.total, a.N, it.n, base, row) : row < a.N;
@@ -829,7 +830,7 @@ __global__ void __launch_bounds__(
       if (shared) mbar_arrive_warp(bar(C::bOFree + 1));
       if (written && h == 0)
         a.lse[lse_at(cu, a.total, it.bh, a.H, a.N, base, row)] =
-            (l > 0.f) ? log2f(l) * 0.69314718055994531f : -INFINITY;
+            (l == 0.f) ? -INFINITY : log2f(l) * 0.69314718055994531f;
     }
   } else {
     // ------------------------------------------------------------------ softmax warps
@@ -1235,7 +1236,8 @@ __global__ void __launch_bounds__(
         break;
       }
       tc_fence_after();
-      float inv_l = (l_run > 0.f) ? 1.f / l_run : 0.f;
+      // (a sum of exactly 0 means no visible key; one that is not a number stays one)
+      float inv_l = (l_run == 0.f) ? 0.f : 1.f / l_run;
       if (kDropout) inv_l *= a.drop.keep_scale;
       if (kFp8) inv_l *= a.o_scale;
       // (the (B*H, N, d) layout forms its row pointer directly: through the packed helpers
@@ -1285,7 +1287,7 @@ __global__ void __launch_bounds__(
       mbar_arrive_warp(bar(C::bOFree + s));
       if (written)
         a.lse[lse_at(cu, a.total, it.bh, a.H, a.N, base, row)] =
-            (l_run > 0.f) ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+            (l_run == 0.f) ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
     }
   }
 

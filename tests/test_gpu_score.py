@@ -179,6 +179,54 @@ def test_bounded_and_unbounded_maxima(d, cap):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=20.0), dict(softcap=60.0), dict(prefix=9),
+                                dict(softcap=20.0, dropout=(0.5, 3, 1)), dict(alibi=True)])
+def test_rows_that_are_no_numbers(d, kw):
+    """A query that is NaN gives an O and an LSE that are, not the LSE of a row without visible
+    keys; the other rows do not notice, and a row whose keys are all padded keeps O = 0 and
+    LSE = -inf."""
+    kw = dict(kw)
+    dev = torch.device("cuda:0")
+    B, H, N = 2, 2, 300
+    q, k, v = (torch.randn(B, H, N, d, device=dev).to(BF16) for _ in range(3))
+    bad = q.clone()
+    rows = [0, 5, 127, 128, 299]
+    bad[1, :, rows] = float("nan")
+    call = dict(causal=True)
+    if "prefix" in kw:
+        call["prefix_lengths"] = torch.tensor([kw.pop("prefix")] * B, dtype=torch.int32, device=dev)
+    if kw.pop("alibi", False):
+        call["alibi_slopes"] = torch.full((H,), 0.1, device=dev)
+    pad = torch.zeros(B, N, dtype=torch.bool, device=dev)
+    pad[0, :10] = True
+    call.update(key_padding=pad, **kw)
+    a, b = (fa.attention_forward(t, k, v, **call) for t in (q, bad))
+    assert torch.isnan(b[1][1][:, rows]).all()
+    assert torch.isnan(b[0][1][:, rows]).all()
+    ok = torch.ones(B, H, N, dtype=torch.bool, device=dev)
+    ok[1, :, rows] = False
+    assert torch.equal(a[1][ok], b[1][ok]) and torch.equal(a[0][ok], b[0][ok])
+    if "prefix_lengths" not in call:
+        assert torch.isneginf(b[1][0, :, :10]).all() and (b[0][0, :, :10] == 0).all()
+    torch.cuda.synchronize()
+    assert fa.fa_debug_status() == 0
+
+
+def test_e4m3_rows_that_are_no_numbers():
+    dev = torch.device("cuda:0")
+    q, k, v = (torch.randn(2, 2, 300, 128, device=dev) for _ in range(3))
+    bad = q.clone()
+    rows = [0, 5, 127, 128, 299]
+    bad[1, :, rows] = float("nan")
+    q, k, v, bad = (t.to(torch.float8_e4m3fn) for t in (q, k, v, bad))
+    a, b = (fa.attention_forward_fp8(t, k, v, causal=True) for t in (q, bad))
+    assert torch.isnan(b[1][1][:, rows]).all() and torch.isnan(b[0][1][:, rows]).all()
+    ok = torch.ones(2, 2, 300, dtype=torch.bool, device=dev)
+    ok[1, :, rows] = False
+    assert torch.equal(a[1][ok], b[1][ok]) and torch.equal(a[0][ok], b[0][ok])
+
+
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("cap", [0.0, 10.0])
 @pytest.mark.parametrize("N", [1, 127, 128, 129, 500])
 def test_prefix(d, cap, N):
