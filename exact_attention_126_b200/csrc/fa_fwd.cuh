@@ -843,9 +843,11 @@ __global__ void __launch_bounds__(
     // what turns a score (kFeatScore with a cap: its tanh) into log2 units
     const float sl2 = kScore && a.cap.on ? a.cap.mul : a.scale_log2;
     int ns = 0;  // S tiles of this stream consumed (all items)
-    // kHalves: key tiles done (each consumed S and published P of either half). One counter in
-    // place of two per half: C5 causal at N 4096, forward 367 -> 350 us
+    // kHalves: key tiles done (each consumed S and published P of either half), and for the e4m3
+    // kernel the same per half. One counter is the faster in the bf16 kernels (B2 H32 N4096 d128
+    // causal: 367 -> 350 us), two per half in the e4m3 one (N8192: 914 us against 956 with one)
     int nt = 0;
+    int nsh[2] = {0, 0}, npub[2] = {0, 0};
     bool ok = true;
 
 
@@ -875,7 +877,8 @@ __global__ void __launch_bounds__(
                           (keep_bits16(a.drop, blk + 1, (uint32_t)row, (uint32_t)it.bh) << 16);
               }
             }
-            if (!mbar_wait_warp(bar((h ? C::bSFull2 : C::bSFull) + s), nt & 1, abort_flag)) {
+            if (!mbar_wait_warp(bar((h ? C::bSFull2 : C::bSFull) + s), (kFp8 ? nsh[h] : nt) & 1,
+                                abort_flag)) {
               ok = false;
               break;
             }
@@ -986,8 +989,8 @@ __global__ void __launch_bounds__(
             // half's P V (the last product into O) has completed
             if (!(j == rg.lo && h == 0) && __any_sync(0xffffffffu, grow)) {
               const int hp = h ^ 1;
-              if (!mbar_wait_warp(bar((hp ? C::bODone2 : C::bODone) + s), (h ? nt : nt - 1) & 1,
-                                  abort_flag)) {
+              if (!mbar_wait_warp(bar((hp ? C::bODone2 : C::bODone) + s),
+                                  (kFp8 ? npub[hp] - 1 : (h ? nt : nt - 1)) & 1, abort_flag)) {
                 ok = false;
                 break;
               }
@@ -1007,6 +1010,10 @@ __global__ void __launch_bounds__(
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive_warp(bar((h ? C::bPFull2 : C::bPFull) + s));
+            if (kFp8) {
+              ++nsh[h];
+              ++npub[h];
+            }
           }
           if (!ok) break;
           ++nt;
@@ -1230,7 +1237,8 @@ __global__ void __launch_bounds__(
       }
       if (!ok) break;
       // epilogue of the item: O / l and LSE, once the last P V product has completed
-      if (!(C::kHalves ? mbar_wait_warp(bar(C::bODone2 + s), (nt - 1) & 1, abort_flag)
+      if (!(C::kHalves ? mbar_wait_warp(bar(C::bODone2 + s), (kFp8 ? npub[1] - 1 : nt - 1) & 1,
+                                        abort_flag)
                        : mbar_wait_warp(bar(C::bODone + s), (ns - 1) & 1, abort_flag))) {
         ok = false;
         break;
