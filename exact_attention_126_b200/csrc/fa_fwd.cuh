@@ -73,6 +73,9 @@ struct FwdArgs {
                              // of the query tile instead of a query tile of its own
   const int* prefix;         // kFeatScore: B prefix lengths, or null
   CapArgs cap;               // kFeatScore: the cap of the scores
+  const __nv_bfloat16* q;    // kFeatNoMax: the tensors behind the maps, for fwd_rows_again
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
 };
 
 // kFp8: 8-bit (e4m3) Q, K, V tiles (head_dim 128 only: one 128-byte row per token). kWide: two
@@ -254,6 +257,106 @@ __device__ __forceinline__ FwdRange fwd_range(const FwdItem& it, int s) {
   return r;
 }
 
+// The sum of the products of eight bf16 pairs.
+__device__ __forceinline__ float dot8(const uint4& x, const uint4& y, float s) {
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    s = fmaf(__uint_as_float(u[e] << 16), __uint_as_float(v[e] << 16), s);
+    s = fmaf(__uint_as_float(u[e] & 0xFFFF0000u), __uint_as_float(v[e] & 0xFFFF0000u), s);
+  }
+  return s;
+}
+
+// Below this a sum without the row's maximum taken off has its weights so low, and below this a sum
+// of products with V is so small, that what underflowed may matter: 2^-40 and 2^-90 (products are
+// lost below 2^-126 each; above either limit O is off by at most N 2^-86, or 2^-36 N of itself).
+constexpr float kLowWeights = 9.094947017729282e-13f;
+constexpr float kLowSums = 8.077935669463161e-28f;
+
+// O of the warp's rows for which `bad` holds, again, for sums of weights without a maximum
+// (kFeatNoMax) that left fp32's range against V: one row after the other by the whole warp, straight
+// from the tensors in fp32, with the row's maximum taken off and the weights divided by their sum
+// before they multiply V. Columns half * D / 2 .. of the row. Values that need this do not occur in
+// a model, so it only has to be right and out of the way: 32 keys at a time, a lane to a key for the
+// scores and to a column for O, and not inlined (B32 H16 N2048 d64 causal, cap 50: 624 us without
+// this, 624 us with it, 630 us inlined).
+template <int D, int kFeat>
+__device__ __noinline__ void fwd_rows_again(const FwdArgs& a, const int* cu, const FwdItem& it, const Mask& mk,
+                               int base, int row, int half, bool bad) {
+  constexpr bool kKpad = (kFeat & kFeatKpad) != 0;
+  constexpr bool kDropout = (kFeat & kFeatDropout) != 0;
+  constexpr int kCols = D / 64;
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (uint32_t todo = __ballot_sync(0xffffffffu, bad); todo != 0; todo &= todo - 1) {
+    const int r = __shfl_sync(0xffffffffu, row, __ffs(todo) - 1);
+    int lo, hi;
+    visible_keys(r, 0, mk.N, mk, lo, hi);
+    const uint4* qr = reinterpret_cast<const uint4*>(a.q + row_at(cu, it.bh, a.H, a.N, base, r, D));
+    // (a packed batch's offsets may point outside the tensor, where rows read as zeros)
+    auto inside = [&](int j) { return cu == nullptr || (base + j >= 0 && base + j < a.total); };
+    auto score = [&](int j) -> float {  // log2 units
+      if (j > hi || (kKpad && a.kpad[(size_t)(it.bh / a.H) * a.N + j] != 0)) return -INFINITY;
+      float s = 0.f;
+      if (inside(j)) {
+        const uint4* kr =
+            reinterpret_cast<const uint4*>(a.k + row_at(cu, it.bh, a.H, a.N, base, j, D));
+#pragma unroll 2
+        for (int i = 0; i < D / 8; ++i) s = dot8(__ldg(qr + i), __ldg(kr + i), s);
+      }
+      return a.cap.mul * tanhf(s * a.cap.scale);
+    };
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+    for (int j0 = lo; j0 <= hi; j0 += 32) {
+      const float y = score(j0 + lane);
+      const float m_new = fmaxf(m, y);
+      if (m_new > -INFINITY) l = l * ex2(m - m_new) + ex2(y - m_new);
+      m = m_new;
+    }
+    float top = m;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    l = m > -INFINITY ? l * ex2(m - top) : 0.f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    const float inv_l = 1.f / l;  // (some key is visible)
+    float acc[kCols];
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
+#pragma unroll 1
+    for (int j0 = lo; j0 <= hi; j0 += 32) {
+      const int key = j0 + lane;
+      float w = ex2(score(key) - top) * inv_l;
+      if (kDropout &&
+          !((keep_bits16(a.drop, (uint32_t)key >> 4, (uint32_t)r, (uint32_t)it.bh) >> (key & 15)) &
+            1u))
+        w = 0.f;
+#pragma unroll 1
+      for (int t = 0; t < 32; ++t) {
+        const float wt = __shfl_sync(0xffffffffu, w, t);
+        if (wt == 0.f || !inside(j0 + t)) continue;
+        const __nv_bfloat16* vr =
+            a.v + row_at(cu, it.bh, a.H, a.N, base, j0 + t, D) + (D / 2) * half + lane;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) acc[c] = fmaf(wt, __bfloat162float(vr[32 * c]), acc[c]);
+      }
+    }
+    const size_t at = row_at(cu, it.bh, a.H, a.N, base, r, D) + (size_t)(D / 2) * half + lane;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+      // (weights of sum 1 keep every partial sum within the largest |V|; dropout's factor may not)
+      if (kDropout) acc[c] *= a.drop.keep_scale;
+      const __nv_bfloat16 o = __float2bfloat16_rn(acc[c]);
+      a.o[at + 32 * c] = o;
+      if (kFeat & kFeatResidual)
+        a.o_low[at + 32 * c] = __float2bfloat16_rn(acc[c] - __bfloat162float(o));
+    }
+  }
+}
+
 // kFeat: kFeatAlibi adds the linear bias -m_h |i - j| (m_h = alibi[bh % H]) to every
 // scaled score; kFeatKpad masks the keys a.kpad flags; kFeatResidual also writes
 // O - bf16(O) to a.o_low; kFeatDropout zeroes the weights whose Philox keep flag is
@@ -269,7 +372,7 @@ template <int D, int kFeat = 0>
 __global__ void __launch_bounds__(
     FwdCfg<D, (kFeat & kFeatFp8) != 0, (kFeat & kFeatNoMax) != 0>::kThreads, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                  const __grid_constant__ CUtensorMap tmV, const FwdArgs a) {
+                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ FwdArgs a) {
   constexpr bool kFp8 = (kFeat & kFeatFp8) != 0;
   constexpr bool kWide = (kFeat & kFeatNoMax) != 0;
   using C = FwdCfg<D, kFp8, kWide>;
@@ -782,6 +885,7 @@ __global__ void __launch_bounds__(
       const bool written = kPacked ? row_written(cu, a.total, a.N, it.n, base, row) : row < a.N;
       const size_t at =
           row_at(cu, it.bh, a.H, a.N, base, written ? row : 0, D) + (size_t)(D / 2) * h;
+      float finite = 0.f, least = INFINITY;  // of the sums: 0 if all are finite; smallest magnitude
 #pragma unroll
       for (int q = 0; q < D / 64; ++q) {
         uint32_t o[32];
@@ -796,6 +900,11 @@ __global__ void __launch_bounds__(
 #pragma unroll
           for (int c = 0; c < 32; ++c)
             o[c] = __float_as_uint(__uint_as_float(o[c]) + __uint_as_float(o2[c]));
+        }
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          finite = fmaf(__uint_as_float(o[c]), 0.f, finite);
+          least = fminf(least, fabsf(__uint_as_float(o[c])));
         }
         uint32_t w[16];
 #pragma unroll
@@ -831,6 +940,13 @@ __global__ void __launch_bounds__(
       if (written && h == 0)
         a.lse[lse_at(cu, a.total, it.bh, a.H, a.N, base, row)] =
             (l == 0.f) ? -INFINITY : log2f(l) * 0.69314718055994531f;
+      // rows with visible keys whose sums overflowed, or lost products to underflow
+      const bool bad =
+          written && l > 0.f && (finite != 0.f || (l < kLowWeights && least < kLowSums));
+      if (__builtin_expect(__any_sync(0xffffffffu, bad), 0)) {
+        __syncwarp();  // the rows as they were are written
+        fwd_rows_again<D, kFeat>(a, cu, it, mk, base, row, h, bad);
+      }
     }
   } else {
     // ------------------------------------------------------------------ softmax warps

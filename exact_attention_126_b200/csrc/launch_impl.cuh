@@ -203,6 +203,9 @@ fa_status_t launch_fwd(const void* q, const void* k, const void* v, void* o, flo
   a.o_scale = x.o_scale;
   a.prefix = x.prefix;
   a.cap = fa::make_cap(x.softcap, scale);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
   const int grid = persistent_grid(a);
   fa::fa_fwd_kernel<D, kFeat><<<grid, C::kThreads, smem, st>>>(mq, mkk, mv, a);
   return launched();

@@ -178,6 +178,117 @@ def test_bounded_and_unbounded_maxima(d, cap):
         assert all(torch.isfinite(out[n]).all() for n in ("dq", "dk", "dv"))
 
 
+def extreme_rows(B, H, N, d, seed):
+    """Queries and keys whose scores reach the cap: rows with every score at -c, every one at +c, and
+    ordinary ones; in odd heads half of the keys at either end."""
+    inp = inputs(B, H, N, d, seed)
+    inp["k"][..., 0] = 64.0
+    inp["q"][:, :, 0::4, 0] = -640.0
+    inp["q"][:, :, 1::4, 0] = 640.0
+    inp["k"][:, 1::2, ::2, 0] = -64.0
+    return inp
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap", [55.0, 50.0, 20.0])
+@pytest.mark.parametrize("B,H,N,mode", [(1, 2, 300, m) for m in (
+    "full", "causal", "window", "pad", "dropout", "padded", "packed")] + [
+        (2, 40, 300, m) for m in ("full", "causal", "packed")])
+def test_values_of_any_size(d, cap, B, H, N, mode):
+    """Sums of the forward that keeps no maximum leave fp32's range against such V and are formed
+    again: query tiles shared by two streams, and one each. The weights of those rows are fp32, so
+    with the residual O is exact to fp32: scores of a few units carry 64 roundings of 2^-24, 4e-5
+    in a weight, and the residual's own rounding 2^-17: 1e-4 in all, asked of the rows whose
+    weights are all 2^(c log2 e) and overflow for certain. Other rows may be of the tensor core's
+    bf16 weights: the plain bound."""
+    inp = extreme_rows(B, H, N, d, 21)
+    dev = torch.device("cuda:0")
+    lens = [N, 140][:B] if mode in ("padded", "packed") else None
+    if lens and B == 1:
+        lens = [211]
+    kw = dict(causal=mode != "full", window=(70, 0) if mode == "window" else (-1, -1))
+    okw = dict(alibi=None, key_padding=None, dropout=None, lengths=lens, softcap=cap)
+    call = dict(softcap=cap, keep_residual=True)
+    if mode == "causal":
+        pre = [100, 0][:B]
+        okw["prefixes"] = pre
+        call["prefix_lengths"] = torch.tensor(pre, dtype=torch.int32, device=dev)
+    if mode == "pad":
+        pad = torch.zeros(B, N, dtype=torch.bool)
+        pad[0, :5] = pad[0, 60:130] = True
+        okw["key_padding"] = pad.numpy().astype(np.uint8)
+        call["key_padding"] = pad.to(dev)
+    if mode == "dropout":
+        okw["dropout"] = call["dropout"] = (0.3, 11, 5)
+    if mode == "padded":
+        call["seq_lengths"] = torch.tensor(lens, dtype=torch.int32, device=dev)
+    if mode == "packed":
+        call.update(cu_seqlens=torch.tensor(cumulative(lens), dtype=torch.int32, device=dev),
+                    max_seqlen=N)
+    put = lambda x: (pack_rows(x, lens) if mode == "packed" else x).to(dev)  # noqa
+    g = torch.Generator().manual_seed(9)
+    sign = torch.where(torch.rand(B, H, N, d, generator=g) < 0.5, -1.0, 1.0)
+    heads = [0, 1] if H <= 2 else [0, 1, H - 1]
+    for size in (3e38, 1e25, 1e15, 1e-30):
+        v = (size * (0.5 + 0.5 * torch.rand(B, H, N, d, generator=g)) * sign).to(BF16)
+        o, lse, low = fa.attention_forward(put(inp["q"]), put(inp["k"]), put(v), 1.0 / d ** 0.5,
+                                           **kw, **call)
+        torch.cuda.synchronize()
+        assert fa.fa_debug_status() == 0
+        f = [synth.to_f64(x[:, heads]) if mode != "dropout" else synth.to_f64(x)
+             for x in (inp["q"], inp["k"], v)]
+        ref, ref_lse = oracle.fwd(*f, 1.0 / d ** 0.5, kw["causal"], kw["window"], **okw)
+        got = o.double().cpu() + low.double().cpu()
+        o, lse = o.double().cpu(), lse.double().cpu()
+        if mode == "packed":
+            c = cumulative(lens)
+            full = [torch.zeros(B, H, N, d, dtype=torch.float64) for _ in range(2)]
+            for b, L in enumerate(lens):
+                for t, x in zip(full, (o, got)):
+                    t[b, :, :L] = x[c[b]:c[b] + L].transpose(0, 1)
+            o, got = full
+            t = torch.full((B, H, N), float("-inf"), dtype=torch.float64)
+            for b, L in enumerate(lens):
+                t[b, :, :L] = lse[:, c[b]:c[b] + L]
+            lse = t
+        o, got, lse = (x[:, heads].numpy() if mode != "dropout" else x.numpy()
+                       for x in (o, got, lse))
+        # (dropout scales kept weights up: what lies past bf16's largest value, 3.39e38, is
+        # infinite; within 2^-7 of it, the bf16 weights' error and the rounding, it may be either)
+        past = np.abs(ref) > 3.39e38 * (1 - 2.0 ** -7)
+        sure = np.abs(ref) > 3.39e38 * (1 + 2.0 ** -7)
+        assert (o[sure] == np.sign(ref[sure]) * np.inf).all() and not (past.any() and size < 3e38)
+        for x in (o, got, ref):
+            x[past] = 0.0
+        for r in range(4):
+            assert rel_frob(o[:, :, r::4] / size, ref[:, :, r::4] / size) < 5e-3, (size, r)
+        dead = np.isneginf(ref_lse)
+        assert np.array_equal(np.isneginf(lse), dead) and (o[dead] == 0).all()
+        assert np.abs(lse[~dead] - ref_lse[~dead]).max() < 1e-3
+        if size >= 1e25 and cap >= 50:
+            assert rel_frob(got[:, ::2, 1::4] / size, ref[:, ::2, 1::4] / size) < 1e-4, size
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_infinite_values_in_masked_places(d):
+    """A value that is infinite, or not a number, reaches the rows that see its key alone."""
+    dev = torch.device("cuda:0")
+    inp = inputs(1, 2, 300, d, 23)
+    inp["v"][0, 0, 200, 3] = float("inf")
+    inp["v"][0, 0, 201, 4] = float("nan")
+    o, lse = fa.attention_forward(*(inp[n].to(dev) for n in "qkv"), 0.125, True, softcap=30.0)
+    f = {n: synth.to_f64(x) for n, x in inp.items()}
+    f["v"][0, 0, 200, 3] = f["v"][0, 0, 201, 4] = 0.0
+    ref, ref_lse = oracle.fwd(f["q"], f["k"], f["v"], 0.125, True, softcap=30.0)
+    o = o.double().cpu().numpy()
+    assert np.abs(lse.double().cpu().numpy() - ref_lse).max() < 1e-3
+    assert np.isposinf(o[0, 0, 200:, 3]).all() and np.isnan(o[0, 0, 201:, 4]).all()
+    o[0, 0, 200:, 3] = ref[0, 0, 200:, 3]
+    o[0, 0, 201:, 4] = ref[0, 0, 201:, 4]
+    assert np.isfinite(o).all() and rel_frob(o, ref) < 5e-3
+    assert rel_frob(o[0, 0, :200], ref[0, 0, :200]) < 5e-3
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("kw", [dict(), dict(softcap=20.0), dict(softcap=60.0), dict(prefix=9),
                                 dict(softcap=20.0, dropout=(0.5, 3, 1)), dict(alibi=True)])
