@@ -723,7 +723,7 @@ def qk_norm_rope_forward(q, k, v=None, q_weight=None, k_weight=None, eps=1e-6, n
     """Queries and keys normalised per head and rotated by their positions, with the values, in
     the layout attention_forward takes. q, k, v: bf16 CUDA tensors (B, N, heads, d) of any token
     and head strides (views of a fused projection), d 64 or 128; returns contiguous
-    (B, heads, N, d) tensors (Q, K), or (Q, K, V) with v. A packed batch (cu_seqlens with
+    (B, heads, N, d) tensors (Q, K), or (Q, K, V) with v; k may be None (then K is). A packed batch (cu_seqlens with
     max_seqlen, as in attention_forward) takes and returns (total, heads, d).
     norm: each row divided by sqrt(mean of squares + eps), times the gain q_weight / k_weight
     (d fp32 values; None = ones). inv_freq (rotary_dim / 2 fp32): rotation p turns values
@@ -775,8 +775,8 @@ def qk_norm_rope_backward(dq, dk, dv=None, q=None, k=None, q_weight=None, k_weig
                           stream=None, out=None):
     """The gradient of qk_norm_rope_forward from those of its outputs, (B, heads, N, d) or packed
     (total, heads, d) (as attention_backward returns them): (gq, gk, gv, gq_weight, gk_weight),
-    gv None without dv, the gains' None for a gain that is None. q, k: the forward's inputs
-    (needed with norm). out: three tensors (the third None without dv) of the forward's input
+    gk and gv None without dk and dv, the gains' None for a gain that is None. q, k: the forward's
+    inputs (needed with norm). out: three tensors (None without dk, dv) of the forward's input
     shapes, of any strides that do not overlap, to write gq, gk, gv to (tokens of a packed batch
     that no sequence covers are left as they are there); by default they are views of one new
     (B, N, heads of all, d) or (total, heads of all, d) tensor, zero for such tokens."""
@@ -798,7 +798,7 @@ def qk_norm_rope_backward(dq, dk, dv=None, q=None, k=None, q_weight=None, k_weig
         raise ValueError("dq must be (B, heads, N, d) or packed (total, heads, d)")
     d, device, at = dq.shape[-1], dq.get_device(), len(tokens)
     grads = [_rows(t, n, tokens, d, device, 1) for t, n in ((dq, "dq"), (dk, "dk"), (dv, "dv"))]
-    if norm and (q is None or k is None):
+    if norm and (q is None or (k is None and dk is not None)):
         raise ValueError("the norm's gradient needs q and k")
     xq = _rows(q, "q", tokens, d, device, at) if norm else None
     xk = _rows(k, "k", tokens, d, device, at) if norm else None
@@ -806,15 +806,15 @@ def qk_norm_rope_backward(dq, dk, dv=None, q=None, k=None, q_weight=None, k_weig
                                      positions, pair_axis, interleaved, seq_lengths, cu_seqlens,
                                      max_seqlen)
     heads = [0 if r is None else r.heads for r in grads]
-    if norm and (xq.heads != heads[0] or xk.heads != heads[1]):
+    if norm and [0 if r is None else r.heads for r in (xq, xk)] != heads[:2]:
         raise ValueError("q and k must have their gradients' heads")
     if out is None:
         out = list(dq.new_empty(tokens + (sum(heads), d)).split(heads, -2))
+        out = [None if r is None else t for t, r in zip(out, grads)]
         params.fill_uncovered = 1
     else:
         out = list(out) + [None] * (3 - len(out))
-    if dv is None:
-        out[2] = None
+        out = [None if r is None else t for t, r in zip(out, grads)]
     outs = [_rows(t, "out", tokens, d, device, at) for t in out]
     if [0 if r is None else r.heads for r in outs] != heads:
         raise ValueError("out must hold tensors of the forward's input shapes")

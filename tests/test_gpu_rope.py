@@ -442,6 +442,42 @@ def test_shared_input_rows():
     assert torch.equal(a[1], b[1].expand(2, 4, 21, 64))
 
 
+@pytest.mark.parametrize("tokens", [(2, 21), (77,), (4, 4100)])
+@pytest.mark.parametrize("values", [False, True])
+def test_queries_without_keys(tokens, values):
+    """A call on queries alone (or with values) gives what the whole call gives for them."""
+    heads = (8, 2, 4)
+    x, kw = make(tokens, heads, 64, 64, 1)
+    call = {}
+    if len(tokens) == 1:
+        call = dict(cu_seqlens=torch.tensor([0, 30, 77], dtype=torch.int32, device=x.device),
+                    max_seqlen=64)
+    q, k, v = x.split(heads, -2)
+    ref = fa.qk_norm_rope_forward(q, k, v, **kw, **call)
+    back = fa.qk_norm_rope_backward(*ref, q=q, k=k, **kw, **call)
+    kw["k_weight"] = None
+    out = fa.qk_norm_rope_forward(q, None, v if values else None, **kw, **call)
+    assert out[1] is None and len(out) == 2 + values
+    assert torch.equal(out[0], ref[0]) and (not values or torch.equal(out[2], ref[2]))
+    got = fa.qk_norm_rope_backward(out[0], None, out[2] if values else None, q=q, **kw, **call)
+    assert got[1] is None and got[4] is None and (got[2] is None) == (not values)
+    assert torch.equal(got[0], back[0]) and (not values or torch.equal(got[2], back[2]))
+    # The gain's gradient is summed over other blocks than in the whole call, so in another order:
+    # both are off by at most rows + 64 roundings of 2^-24 of the sum of the terms' magnitudes, and
+    # a term is a turned dy (at most the norm of its two members, here sqrt(2) max |dy|) times x^
+    # (at most sqrt(64)).
+    rows = ref[0].numel() // 64
+    most = rows * 2.0 ** 0.5 * float(ref[0].float().abs().max()) * 8.0
+    assert float((got[3] - back[3]).abs().max()) <= 2 * (rows + 64) * 2.0 ** -24 * most
+    given = [torch.empty_like(q), None, torch.empty_like(v) if values else None]
+    again = fa.qk_norm_rope_backward(out[0], None, out[2] if values else None, q=q, out=given,
+                                     **kw, **call)
+    if len(tokens) == 2:
+        assert again[0] is given[0] and torch.equal(again[0], got[0])
+    with pytest.raises(ValueError):
+        fa.qk_norm_rope_backward(ref[0], ref[1], q=q, **kw, **call)
+
+
 def test_in_place():
     x, kw = make((77,), (4, 2, 2), 128, 64, 1)
     cu = torch.tensor([0, 30, 77], dtype=torch.int32, device=x.device)
