@@ -469,16 +469,24 @@ def _check_inputs(*ts):
             raise ValueError("q, k, v (and dO) must share one shape")
 
 
+def _check_device(t, name, q):
+    """The kernels read `t` by its address on the queries' device."""
+    if t.get_device() != q.get_device():
+        raise ValueError("%s must be on the queries' device" % name)
+
+
 def _check_slopes(alibi_slopes, q):
     if not alibi_slopes.is_cuda or alibi_slopes.dtype != torch.float32:
         raise ValueError("alibi_slopes must be an fp32 CUDA tensor")
+    _check_device(alibi_slopes, "alibi_slopes", q)
     if alibi_slopes.numel() != q.shape[1] or not alibi_slopes.is_contiguous():
         raise ValueError("alibi_slopes must hold one slope per head, contiguous")
 
 
-def _check_padding(key_padding, B, N):
+def _check_padding(key_padding, q, B, N):
     if not key_padding.is_cuda or key_padding.dtype not in (torch.bool, torch.uint8):
         raise ValueError("key_padding must be a bool or uint8 CUDA tensor")
+    _check_device(key_padding, "key_padding", q)
     if tuple(key_padding.shape) != (B, N) or not key_padding.is_contiguous():
         raise ValueError("key_padding must be a contiguous (batch, seq_len) tensor")
 
@@ -486,6 +494,7 @@ def _check_padding(key_padding, B, N):
 def _check_lengths(seq_lengths, q):
     if not seq_lengths.is_cuda or seq_lengths.dtype != torch.int32:
         raise ValueError("seq_lengths must be an int32 CUDA tensor")
+    _check_device(seq_lengths, "seq_lengths", q)
     if seq_lengths.numel() != q.shape[0] or not seq_lengths.is_contiguous():
         raise ValueError("seq_lengths must hold one length per batch entry, contiguous")
 
@@ -496,6 +505,7 @@ def _packed_dims(q, cu_seqlens, max_seqlen, seq_lengths):
         raise ValueError("seq_lengths and cu_seqlens exclude each other")
     if not cu_seqlens.is_cuda or cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1:
         raise ValueError("cu_seqlens must be a 1-D int32 CUDA tensor")
+    _check_device(cu_seqlens, "cu_seqlens", q)
     if cu_seqlens.numel() < 2 or not cu_seqlens.is_contiguous():
         raise ValueError("cu_seqlens must hold B + 1 >= 2 offsets, contiguous")
     if q.dim() != 3:
@@ -512,8 +522,7 @@ def _score(softcap, prefix_lengths, q, B):
             raise ValueError("prefix_lengths must be an int32 CUDA tensor")
         if tuple(prefix_lengths.shape) != (B,) or not prefix_lengths.is_contiguous():
             raise ValueError("prefix_lengths must hold one length per sequence, contiguous")
-        if prefix_lengths.device != q.device:
-            raise ValueError("prefix_lengths must be on the queries' device")
+        _check_device(prefix_lengths, "prefix_lengths", q)
     elif softcap is None or softcap == 0.0:
         return None
     return fa_score_t(_ptr(prefix_lengths), 0.0 if softcap is None else float(softcap))
@@ -560,7 +569,7 @@ def attention_forward(q, k, v, scale=None, causal=False, window=(-1, -1), stream
     if alibi_slopes is not None:
         _check_slopes(alibi_slopes, q)
     if key_padding is not None:
-        _check_padding(key_padding, B, N)
+        _check_padding(key_padding, q, B, N)
     if seq_lengths is not None:
         _check_lengths(seq_lengths, q)
     score = _score(softcap, prefix_lengths, q, B)
@@ -612,7 +621,7 @@ def attention_backward(q, k, v, o, lse, do, scale=None, causal=False, window=(-1
     if alibi_slopes is not None:
         _check_slopes(alibi_slopes, q)
     if key_padding is not None:
-        _check_padding(key_padding, B, N)
+        _check_padding(key_padding, q, B, N)
     if o_low is not None:
         _check_inputs(q, o_low)
     if seq_lengths is not None:
