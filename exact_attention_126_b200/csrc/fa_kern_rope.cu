@@ -10,11 +10,26 @@ namespace fa_host {
 
 namespace {
 
-// From how many bytes of rows the tile kernel runs. Measured against the row kernels (d = 64, 3 x 16
-// heads / d = 128, 32 + 2 x 8 heads, one sequence): forward 18.4 us either way at 25 MB, 28.7 -> 24.6
-// / 28.7 -> 30.7 at 50 MB, 84 -> 76 / 82 -> 82 at 201 MB; backward 28.7 either way / 30 -> 33, 47 ->
-// 39 / 45 -> 44 and 133 -> 104 / 131 -> 119.
-constexpr long long kTileMinBytes = 32ll << 20;
+// When the tile kernel runs, by the bytes of rows and the share of its tiles' token slots that hold
+// a row (a sequence's last tile may hold few). Row / tile kernel in us, inputs from memory, kernels
+// alone (3 x 16 heads of 64; 32 + 2 x 8 heads of 128):
+//   one sequence     33 MB       50 MB       100 MB      200 MB      400 MB
+//   d 64  forward    17 / 16     24 / 22     45 / 40     87 / 78    166 / 148
+//         backward   29 / 24     40 / 34     72 / 58    134 / 104   254 / 196
+//   d 128 forward    20 / 21     24 / 26     46 / 45     84 / 80    161 / 148
+//         backward   34 / 31     39 / 38     72 / 65    131 / 116   251 / 211
+//   short ones, 200 MB (share)   forward     backward
+//   d 64   N 33  (52%)           85 / 121    133 / 172
+//          N 65  (68%)           85 / 95     133 / 130
+//          N 257 (89%)           82 / 80     129 / 109
+//   d 128  N 17  (53%)           82 / 135    131 / 195
+//          N 65  (81%)           82 / 92     131 / 131
+//          N 257 (94%)           82 / 82     131 / 118
+template <int D, bool kBwd>
+bool tiles_pay(long long bytes, long long rows, long long slots) {
+  constexpr long long kMinBytes = (D == 128 && !kBwd ? 96ll : 32ll) << 20;
+  return bytes >= kMinBytes && 8 * rows >= 7 * slots;
+}
 
 // SMs of the current device (asked once per device).
 int device_sms() {
@@ -69,7 +84,7 @@ bool rows_map(CUtensorMap* map, const fa::HeadRows& r, const fa::RopeArgs& a, in
 }
 
 // Launches the tile kernel if the problem is one for it: sequences of at least a tile of tokens,
-// kTileMinBytes of rows, strides that a tensor map takes. Returns its blocks, 0 if it was not
+// rows as tiles_pay has them, strides that a tensor map takes. Returns its blocks, 0 if it was not
 // launched, -1 on an error.
 template <int D, bool kInter, bool kBwd>
 int tiles(const fa::RopeArgs& a, cudaStream_t st) {
@@ -83,7 +98,7 @@ int tiles(const fa::RopeArgs& a, cudaStream_t st) {
     bytes += (long long)a.tokens * y.heads * D * 2;
     if (y.heads > 0) items += per_kind;
   }
-  if (rows < T::kTokens || bytes < kTileMinBytes) return 0;
+  if (rows < T::kTokens || !tiles_pay<D, kBwd>(bytes, a.tokens, per_kind * T::kTokens)) return 0;
   fa::RopeMaps m;
   for (int i = 0; i < 3; ++i) {
     if (a.y[i].heads == 0) continue;

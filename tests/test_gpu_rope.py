@@ -212,6 +212,50 @@ def test_tiles(d, heads, interleaved, rot, axes, norm):
     check(x, heads, kw, interleaved, norm=norm)
 
 
+# (the forward at d 128 takes tiles from 96 MB on)
+@pytest.mark.parametrize("interleaved,rot,axes,norm", [(False, None, 1, True), (True, 24, 3, True),
+                                                       (False, None, 2, False)])
+def test_tiles_of_a_large_batch(interleaved, rot, axes, norm):
+    d, heads = 128, (21, 6, 5)
+    x, kw = make((3, 4333), heads, d, d if rot is None else rot, axes, gains=norm)
+    assert x.numel() * 2 > 97 << 20
+    check(x, heads, kw, interleaved, norm=norm)
+
+
+@pytest.mark.parametrize("padded", [True, False])
+def test_tiles_of_a_large_batch_of_lengths(padded):
+    d, heads = 128, (21, 6, 5)
+    if padded:
+        N, lens = 2111, [2111, 0, 33, 1, 5000, 2048]
+        x, kw = make((6, N), heads, d, d, 1)
+        live = (np.arange(N) < np.array(lens)[:, None]).reshape(-1)
+        x[torch.from_numpy(~live.reshape(6, N))] = float("nan")
+        check(x, heads, kw, live=live, eps=0.0,
+              seq_lengths=torch.tensor(lens, dtype=torch.int32, device=x.device))
+    else:
+        lens, first, total, N = [5, 0, 5400, 1, 0, 4900, 2000, 0], 37, 12600, 5000
+        cu = first + np.concatenate([[0], np.cumsum(lens)])
+        x, kw = make((total,), heads, d, d, 1)
+        live, places = np.zeros(total, bool), np.zeros(total)
+        for b, n in enumerate(lens):
+            live[cu[b]:cu[b] + min(n, N)] = True
+            places[cu[b]:cu[b] + n] = np.arange(n)
+        x[torch.from_numpy(~live)] = float("inf")
+        check(x, heads, kw, live=live, places=places, max_seqlen=N,
+              cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=x.device))
+    assert x.numel() * 2 > 97 << 20
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N", [17, 33, 65, 257])
+def test_large_batches_of_short_sequences(d, N):
+    """Either side of the rule that keeps tiles of few rows out."""
+    heads = (9, 4, 3) if d == 64 else (4, 2, 2)
+    x, kw = make((33000 // N, N), heads, d, d, 1)
+    assert x.numel() * 2 > 33 << 20
+    check(x, heads, kw)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_tiles_of_a_padded_batch(d):
     B, N, heads = 7, 2705, (6, 5, 4)
