@@ -1170,7 +1170,7 @@ __global__ void __launch_bounds__(
             float y[32];
 #pragma unroll
             for (int c = 0; c < 32; ++c) y[c] = __uint_as_float(u[c]);
-            if (a.cap.on) cap_tanh(y, a.cap);
+            cap_tanh(y, a.cap);
             if (kAlibi) {
               const float base = (float)((long long)j * kBlock + 32 * q - row);
 #pragma unroll
