@@ -267,9 +267,9 @@ fa_status_t forward(const void* q, const void* k, const void* v, void* o, float*
   const int l = window.left, BH = B * H;
   const Problem pb{BH, H, N, scale, l, right};
   const int fault = g_fault.load(std::memory_order_relaxed);
-  s = d == 64 ? dispatch_features<FwdLaunch<64>>(FwdFeatures64(), x.features(), q, k, v, o, lse,
+  s = d == 64 ? dispatch_features<FwdLaunch<64>>(FwdFeatures64(), x.features(N), q, k, v, o, lse,
                                                  pb, x, fault, st)
-              : dispatch_features<FwdLaunch<128>>(FwdFeatures128(), x.features(), q, k, v, o,
+              : dispatch_features<FwdLaunch<128>>(FwdFeatures128(), x.features(N), q, k, v, o,
                                                   lse, pb, x, fault, st);
   if (s != FA_OK || x.seq_len == nullptr) return s;
   return fill(o, x.o_low, nullptr, lse, d, BH, H, N, x, st);
@@ -310,7 +310,7 @@ fa_status_t fused_pass(const void* q, const void* k, const void* v, const void* 
   const int right = fa::resolve_right(causal, window.right);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const Problem pb{B * H, H, N, scale, window.left, right};
-  const int feat = x.features() & ~(fa::kFeatResidual | fa::kFeatNoMax);
+  const int feat = x.features(N) & ~(fa::kFeatResidual | fa::kFeatNoMax);
   const Extras xs = with_sched(x, workspace, B, H, N, d);
   s = dispatch_features<FusedLaunch>(FusedFeatures(), feat, q, k, v, dout, workspace,
                                      dq_acc_of(workspace, B, H, N), dk, dv, pb, xs, st);
@@ -345,7 +345,7 @@ fa_status_t dkdv_pass(const void* q, const void* k, const void* v, const void* d
   const int right = fa::resolve_right(causal, window.right);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int l = window.left, BH = B * H;
-  const int feat = x.features() & ~(fa::kFeatResidual | fa::kFeatNoMax);
+  const int feat = x.features(N) & ~(fa::kFeatResidual | fa::kFeatNoMax);
   const Problem pb{BH, H, N, scale, l, right};
   const Extras xs = with_sched(x, workspace, B, H, N, d);
   s = d == 64 ? dispatch_features<DkdvLaunch<64>>(BwdFeatures(), feat, q, k, v, dout, workspace,
@@ -368,7 +368,7 @@ fa_status_t dq_pass(const void* q, const void* k, const void* v, const void* dou
   const int right = fa::resolve_right(causal, window.right);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int l = window.left, BH = B * H;
-  const int feat = x.features() & ~(fa::kFeatResidual | fa::kFeatNoMax);
+  const int feat = x.features(N) & ~(fa::kFeatResidual | fa::kFeatNoMax);
   const Problem pb{BH, H, N, scale, l, right};
   const Extras xs = with_sched(x, workspace, B, H, N, d);
   s = d == 64 ? dispatch_features<DqLaunch<64>>(BwdFeatures(), feat, q, k, v, dout, workspace,

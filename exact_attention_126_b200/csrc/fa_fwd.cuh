@@ -268,91 +268,159 @@ __device__ __forceinline__ float dot8(const uint4& x, const uint4& y, float s) {
   return s;
 }
 
-// Below this a sum without the row's maximum taken off has its weights so low, and below this a sum
-// of products with V is so small, that what underflowed may matter: 2^-40 and 2^-90 (products are
-// lost below 2^-126 each; above either limit O is off by at most N 2^-86, or 2^-36 N of itself).
+// Sums of weights (2^-40) and of their products with V (2^-90) below which, both at once, what
+// underflowed may matter: products are lost below 2^-126 each, so that above the one limit O is off
+// by at most N 2^-86, above the other by N 2^-36 of itself.
 constexpr float kLowWeights = 9.094947017729282e-13f;
 constexpr float kLowSums = 8.077935669463161e-28f;
 
-// O of the warp's rows for which `bad` holds, again, for sums of weights without a maximum
-// (kFeatNoMax) that left fp32's range against V: one row after the other by the whole warp, straight
-// from the tensors in fp32, with the row's maximum taken off and the weights divided by their sum
-// before they multiply V. Columns half * D / 2 .. of the row. Values that need this do not occur in
-// a model, so it only has to be right and out of the way: 32 keys at a time, a lane to a key for the
-// scores and to a column for O, and not inlined (B32 H16 N2048 d64 causal, cap 50: 624 us without
-// this, 624 us with it, 630 us inlined).
+// O, again, of those of the warp's rows (a lane to a row) whose sums without a maximum (kFeatNoMax)
+// left fp32's range against V: `over`, or with the weights' sum and what O became of it so low that
+// products were lost (no row where `sum` is 0). Two rows at a time by the whole warp, straight from
+// the tensors in fp32, with the row's maximum taken off and the weights divided by their sum before
+// they multiply V. Columns half * D / 2 .. of the row. Values that need this do not occur in a model,
+// so it only has to be right and out of the way: 32 keys at a time, a lane to a key for the scores and
+// to a column for O, and not inlined (B32 H16 N2048 d64 causal, cap 50: 624 us without this, 629 us
+// with it; B2 H32 N4096 d128 362 and 364. With four rows at a time its registers made the kernel spill:
+// with the residual 643 -> 655 and 383 -> 395 us).
 template <int D, int kFeat>
-__device__ __noinline__ void fwd_rows_again(const FwdArgs& a, const int* cu, const FwdItem& it, const Mask& mk,
-                               int base, int row, int half, bool bad) {
+__device__ __noinline__ void fwd_rows_again(const FwdArgs& a, int bh, int n, int prefix, int row,
+                                            int half, float sum, bool over) {
   constexpr bool kKpad = (kFeat & kFeatKpad) != 0;
   constexpr bool kDropout = (kFeat & kFeatDropout) != 0;
+  const int* const cu = (kFeat & kFeatPacked) ? a.cu : nullptr;
+  const int base = seq_base(cu, bh, a.H);
+  const Mask mk{n, a.left, a.right, prefix};
   constexpr int kCols = D / 64;
+  constexpr int R = 2;
   const int lane = threadIdx.x & 31;
+  bool bad = sum > 0.f && over;
+  if (sum > 0.f && sum < kLowWeights && !over) {
+    const uint4* o =
+        reinterpret_cast<const uint4*>(a.o + row_at(cu, bh, a.H, a.N, base, row, D) + (D / 2) * half);
+    float least = INFINITY;
 #pragma unroll 1
-  for (uint32_t todo = __ballot_sync(0xffffffffu, bad); todo != 0; todo &= todo - 1) {
-    const int r = __shfl_sync(0xffffffffu, row, __ffs(todo) - 1);
-    int lo, hi;
-    visible_keys(r, 0, mk.N, mk, lo, hi);
-    const uint4* qr = reinterpret_cast<const uint4*>(a.q + row_at(cu, it.bh, a.H, a.N, base, r, D));
-    // (a packed batch's offsets may point outside the tensor, where rows read as zeros)
-    auto inside = [&](int j) { return cu == nullptr || (base + j >= 0 && base + j < a.total); };
-    auto score = [&](int j) -> float {  // log2 units
-      if (j > hi || (kKpad && a.kpad[(size_t)(it.bh / a.H) * a.N + j] != 0)) return -INFINITY;
-      float s = 0.f;
-      if (inside(j)) {
-        const uint4* kr =
-            reinterpret_cast<const uint4*>(a.k + row_at(cu, it.bh, a.H, a.N, base, j, D));
-#pragma unroll 2
-        for (int i = 0; i < D / 8; ++i) s = dot8(__ldg(qr + i), __ldg(kr + i), s);
-      }
-      return a.cap.mul * tanhf(s * a.cap.scale);
-    };
-    float m = -INFINITY, l = 0.f;
-#pragma unroll 1
-    for (int j0 = lo; j0 <= hi; j0 += 32) {
-      const float y = score(j0 + lane);
-      const float m_new = fmaxf(m, y);
-      if (m_new > -INFINITY) l = l * ex2(m - m_new) + ex2(y - m_new);
-      m = m_new;
+    for (int i = 0; i < D / 16; ++i) {
+      const uint4 x = o[i];
+      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        least = fminf(least, fminf(fabsf(__uint_as_float(u[e] << 16)),
+                                   fabsf(__uint_as_float(u[e] & 0xFFFF0000u))));
     }
-    float top = m;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    l = m > -INFINITY ? l * ex2(m - top) : 0.f;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-    const float inv_l = 1.f / l;  // (some key is visible)
-    float acc[kCols];
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
+    bad = least * sum < kLowSums;
+  }
+  __syncwarp();  // (the rows as they were are written, by their own lanes)
+  // (a packed batch's offsets may point outside the tensor, where rows read as zeros)
+  auto inside = [&](int j) { return cu == nullptr || (base + j >= 0 && base + j < a.total); };
 #pragma unroll 1
-    for (int j0 = lo; j0 <= hi; j0 += 32) {
+  for (uint32_t todo = __ballot_sync(0xffffffffu, bad); todo != 0;) {
+    int r[R], lo[R], hi[R], first = mk.N, last = -1;
+    const uint4* qr[R];
+    float m[R], l[R], acc[R][kCols];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      // (past the last one: that one once more)
+      r[i] = __shfl_sync(0xffffffffu, row, todo != 0 ? __ffs(todo) - 1 : 0);
+      if (todo == 0 && i > 0) r[i] = r[i - 1];
+      todo &= todo - 1;
+      visible_keys(r[i], 0, mk.N, mk, lo[i], hi[i]);
+      first = lo[i] < first ? lo[i] : first;
+      last = hi[i] > last ? hi[i] : last;
+      qr[i] = reinterpret_cast<const uint4*>(a.q + row_at(cu, bh, a.H, a.N, base, r[i], D));
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) acc[i][c] = 0.f;
+    }
+    // the rows' scores of key j in log2 units, -inf where it is masked
+    auto scores = [&](int j, float (&y)[R]) {
+      float s[R] = {};
+      if (j <= last && inside(j)) {
+        const uint4* kr =
+            reinterpret_cast<const uint4*>(a.k + row_at(cu, bh, a.H, a.N, base, j, D));
+#pragma unroll 1
+        for (int e = 0; e < D / 8; ++e) {
+          const uint4 x = __ldg(kr + e);
+#pragma unroll
+          for (int i = 0; i < R; ++i) s[i] = dot8(__ldg(qr[i] + e), x, s[i]);
+        }
+      }
+      const bool padded = kKpad && j <= last && a.kpad[(size_t)(bh / a.H) * a.N + j] != 0;
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        y[i] = !padded && j >= lo[i] && j <= hi[i] ? a.cap.mul * tanhf(s[i] * a.cap.scale)
+                                                   : -INFINITY;
+    };
+#pragma unroll 1
+    for (int j0 = first; j0 <= last; j0 += 32) {
+      float y[R];
+      scores(j0 + lane, y);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const float m_new = fmaxf(m[i], y[i]);
+        if (m_new > -INFINITY) l[i] = l[i] * ex2(m[i] - m_new) + ex2(y[i] - m_new);
+        m[i] = m_new;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      float top = m[i];
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      float sum = m[i] > -INFINITY ? l[i] * ex2(m[i] - top) : 0.f;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      m[i] = top;
+      l[i] = 1.f / sum;  // (some key is visible)
+    }
+#pragma unroll 1
+    for (int j0 = first; j0 <= last; j0 += 32) {
       const int key = j0 + lane;
-      float w = ex2(score(key) - top) * inv_l;
-      if (kDropout &&
-          !((keep_bits16(a.drop, (uint32_t)key >> 4, (uint32_t)r, (uint32_t)it.bh) >> (key & 15)) &
-            1u))
-        w = 0.f;
+      float w[R];
+      scores(key, w);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        w[i] = ex2(w[i] - m[i]) * l[i];
+        if (kDropout && !((keep_bits16(a.drop, (uint32_t)key >> 4, (uint32_t)r[i],
+                                       (uint32_t)bh) >> (key & 15)) & 1u))
+          w[i] = 0.f;
+      }
 #pragma unroll 1
       for (int t = 0; t < 32; ++t) {
-        const float wt = __shfl_sync(0xffffffffu, w, t);
-        if (wt == 0.f || !inside(j0 + t)) continue;
-        const __nv_bfloat16* vr =
-            a.v + row_at(cu, it.bh, a.H, a.N, base, j0 + t, D) + (D / 2) * half + lane;
+        float wt[R];
+        bool any = false;
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) acc[c] = fmaf(wt, __bfloat162float(vr[32 * c]), acc[c]);
+        for (int i = 0; i < R; ++i) {
+          wt[i] = __shfl_sync(0xffffffffu, w[i], t);
+          any = any || wt[i] != 0.f;
+        }
+        if (!any || !inside(j0 + t)) continue;
+        const __nv_bfloat16* vr =
+            a.v + row_at(cu, bh, a.H, a.N, base, j0 + t, D) + (D / 2) * half + lane;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+          const float x = __bfloat162float(vr[32 * c]);
+#pragma unroll
+          for (int i = 0; i < R; ++i)  // (a key that a row does not see may hold an infinity)
+            acc[i][c] = wt[i] != 0.f ? fmaf(wt[i], x, acc[i][c]) : acc[i][c];
+        }
       }
     }
-    const size_t at = row_at(cu, it.bh, a.H, a.N, base, r, D) + (size_t)(D / 2) * half + lane;
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) {
-      // (weights of sum 1 keep every partial sum within the largest |V|; dropout's factor may not)
-      if (kDropout) acc[c] *= a.drop.keep_scale;
-      const __nv_bfloat16 o = __float2bfloat16_rn(acc[c]);
-      a.o[at + 32 * c] = o;
-      if (kFeat & kFeatResidual)
-        a.o_low[at + 32 * c] = __float2bfloat16_rn(acc[c] - __bfloat162float(o));
+    for (int i = 0; i < R; ++i) {
+      const size_t at =
+          row_at(cu, bh, a.H, a.N, base, r[i], D) + (size_t)(D / 2) * half + lane;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        // (weights of sum 1 keep every partial sum within the largest |V|; dropout's factor may not)
+        if (kDropout) acc[i][c] *= a.drop.keep_scale;
+        const __nv_bfloat16 o = __float2bfloat16_rn(acc[i][c]);
+        a.o[at + 32 * c] = o;
+        if (kFeat & kFeatResidual)
+          a.o_low[at + 32 * c] = __float2bfloat16_rn(acc[i][c] - __bfloat162float(o));
+      }
     }
   }
 }
@@ -885,8 +953,8 @@ __global__ void __launch_bounds__(
       const bool written = kPacked ? row_written(cu, a.total, a.N, it.n, base, row) : row < a.N;
       const size_t at =
           row_at(cu, it.bh, a.H, a.N, base, written ? row : 0, D) + (size_t)(D / 2) * h;
-      float finite = 0.f, least = INFINITY;  // of the sums: 0 if all are finite; smallest magnitude
-#pragma unroll
+      bool over = false;  // some sum is not finite
+#pragma unroll 1
       for (int q = 0; q < D / 64; ++q) {
         uint32_t o[32];
         tmem_ld32(tO + 32 * q, o);
@@ -901,11 +969,12 @@ __global__ void __launch_bounds__(
           for (int c = 0; c < 32; ++c)
             o[c] = __float_as_uint(__uint_as_float(o[c]) + __uint_as_float(o2[c]));
         }
+        float2 finite = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          finite = fmaf(__uint_as_float(o[c]), 0.f, finite);
-          least = fminf(least, fabsf(__uint_as_float(o[c])));
-        }
+        for (int c = 0; c < 32; c += 2)
+          finite = __ffma2_rn(make_float2(__uint_as_float(o[c]), __uint_as_float(o[c + 1])),
+                              make_float2(0.f, 0.f), finite);
+        over = over || finite.x + finite.y != 0.f;
         uint32_t w[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c)
@@ -940,13 +1009,9 @@ __global__ void __launch_bounds__(
       if (written && h == 0)
         a.lse[lse_at(cu, a.total, it.bh, a.H, a.N, base, row)] =
             (l == 0.f) ? -INFINITY : log2f(l) * 0.69314718055994531f;
-      // rows with visible keys whose sums overflowed, or lost products to underflow
-      const bool bad =
-          written && l > 0.f && (finite != 0.f || (l < kLowWeights && least < kLowSums));
-      if (__builtin_expect(__any_sync(0xffffffffu, bad), 0)) {
-        __syncwarp();  // the rows as they were are written
-        fwd_rows_again<D, kFeat>(a, cu, it, mk, base, row, h, bad);
-      }
+      // rows with visible keys whose sums overflowed, or may have lost products to underflow
+      if (__builtin_expect(__any_sync(0xffffffffu, l > 0.f && (over || l < kLowWeights)), 0))
+        fwd_rows_again<D, kFeat>(a, it.bh, it.n, it.prefix, row, h, written ? l : 0.f, over);
     }
   } else {
     // ------------------------------------------------------------------ softmax warps

@@ -39,18 +39,19 @@ struct Extras {
   bool scored() const { return prefix != nullptr || softcap > 0.f; }
 
   // Scores so far bounded by the cap that the forward keeps no running maximum (a bias is not
-  // bounded).
-  bool no_max() const {
-    return softcap > 0.f && softcap * fa::kLog2e <= fa::kCapNoMax && alibi == nullptr;
+  // bounded), in sequences short enough for what fwd_rows_again may have to do.
+  bool no_max(int N) const {
+    return softcap > 0.f && softcap * fa::kLog2e <= fa::kCapNoMax && alibi == nullptr &&
+           N <= fa::kNoMaxKeys;
   }
 
-  // The kernel variant these options select (the backward passes ignore kFeatResidual and
-  // kFeatNoMax).
-  int features() const {
+  // The kernel variant these options select for sequences of N rows (the backward passes ignore
+  // kFeatResidual and kFeatNoMax).
+  int features(int N) const {
     return (alibi ? fa::kFeatAlibi : 0) | (kpad ? fa::kFeatKpad : 0) |
            (o_low ? fa::kFeatResidual : 0) | (dropout ? fa::kFeatDropout : 0) |
            (fp8 ? fa::kFeatFp8 : 0) | (cu ? fa::kFeatPacked : 0) |
-           (scored() ? fa::kFeatScore : 0) | (no_max() ? fa::kFeatNoMax : 0);
+           (scored() ? fa::kFeatScore : 0) | (no_max(N) ? fa::kFeatNoMax : 0);
   }
 };
 

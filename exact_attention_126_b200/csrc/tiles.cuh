@@ -31,6 +31,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 // stay far inside fp32's (and bf16's) exponents as they are.
 constexpr float kCapNoMax = 80.f;
 
+// The longest sequence for which it goes without: were every row of a CTA's query tiles to be formed
+// again (fwd_rows_again), that takes 1.05 s at this length (head_dim 128, every key
+// visible), and the CTA's other warps wait for at most 2 s. (What a maximum costs there: B1
+// H4 causal, cap 50, 65537 keys 5.96 ms against 4.32 ms of 65536 without one at head_dim 64, 5.37
+// against 4.91 ms at 128.)
+constexpr int kNoMaxKeys = 98304;
+
 struct Mask {
   int N;      // sequence length
   int left;   // -1 = unbounded

@@ -545,8 +545,8 @@ def attention_forward(q, k, v, scale=None, causal=False, window=(-1, -1), stream
     batch, q, k, v of shape (total, H, d) holding sequence b at tokens cu_seqlens[b] ..
     cu_seqlens[b+1]-1; O is (total, H, d) and LSE (H, total), not written for tokens that no
     sequence covers (nor are their gradients by attention_backward). softcap (c > 0): the scaled scores
-    s become c tanh(s / c) (with c up to 55, N max|V| must stay below 1e14). prefix_lengths ((B,) int32), for causal problems: query i of
-    sequence b also sees every key j < prefix_lengths[b]."""
+    s become c tanh(s / c). prefix_lengths ((B,) int32), for causal problems: query i of sequence b
+    also sees every key j < prefix_lengths[b]."""
     if _elsewhere(q):
         with torch.cuda.device(q.device):
             return attention_forward(q, k, v, scale, causal, window, stream, alibi_slopes,

@@ -28,6 +28,7 @@
  * Scale.  scale multiplies Q K^T before the mask. It is used exactly as given and
  *   must be finite and > 0 (else FA_ERR_INVALID_ARG); pass 1/sqrt(d) for the usual
  *   default (`softmax_scale=None`, page "告别OOM和训练慢…" §4.2).
+ * Values.  O's fp32 sums are of weights up to 2^8 times V: they hold 2^8 N max|V| up to 3.4e38.
  * Mask.  Key j is visible from query i iff
  *     (window.left  < 0 or j >= i - window.left) and
  *     (window.right < 0 or j <= i + window.right),
@@ -217,8 +218,11 @@ fa_status_t fa_fwd_fp8(const void *q, const void *k, const void *v, float q_scal
  *   softcap  c > 0 caps the scaled scores s: they become c tanh(s / c), before an ALiBi bias, the
  *            mask and the softmax (LSE is that of the capped scores); 0 = no cap. c in
  *            [1e-30, 1e30] and scale / c in [1e-6, 1e6] (else FA_ERR_INVALID_ARG). With a cap of
- *            at most 55 and no bias, the fp32 sums behind O are of exp(score) V as it is, without
- *            the row's maximum taken off: N max|V| must stay below 1e14, else O overflows.
+ *            at most 80 ln 2 (55.45), no bias and N up to 98304, the fp32 sums behind O are of
+ *            exp(score) V as it is, without the row's maximum taken off. Rows whose sums leave
+ *            fp32's range (N max|V| above about 1e14 where scores lie at the cap; V below 1e-14
+ *            where they all lie at its negative) are formed again, each for itself: right, but
+ *            some hundred times slower.
  */
 typedef struct {
     const int *prefix_lengths;
@@ -441,13 +445,14 @@ typedef struct {
  *               as axes - 1), or NULL if there is one axis.
  *   positions   (axes, B, N) int32, packed (axes, total_tokens); or NULL with one axis: each
  *               token's place in its sequence.
- *   seq_lengths B int32 real lengths of a padded batch, or NULL: rows past a length are not
- *               read, get zeros, and add nothing to the gains' gradients.
+ *   seq_lengths B int32 real lengths of a padded batch, or NULL: rows past a length do not
+ *               enter the results (they may be read), get zeros, and add nothing to the gains'
+ *               gradients.
  *   cu_seqlens, total_tokens
  *               a packed batch as in fa_options_t, or NULL / 0; offsets must not decrease. N is
  *               the longest sequence handled. Tokens that no sequence covers (before the first,
- *               behind the last, past N) do not enter the results and are not written, unless
- *               fill_uncovered asks for it. Exclusive with seq_lengths (FA_ERR_INVALID_ARG).
+ *               behind the last, past N) do not enter the results (they may be read) and are
+ *               not written, unless fill_uncovered asks for it. Exclusive with seq_lengths (FA_ERR_INVALID_ARG).
  *   eps         finite, >= 0.
  *   rotary_dim  a multiple of 8 in [0, d] (else FA_ERR_UNSUPPORTED); 0: no rotation.
  *   axes        1 .. FA_MAX_AXES (above: FA_ERR_UNSUPPORTED); not looked at without rotation.

@@ -270,6 +270,25 @@ def test_values_of_any_size(d, cap, B, H, N, mode):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N,size", [(98304, 2e38), (98304, 1e30), (98305, 1e30)])
+def test_values_of_any_size_in_long_sequences(d, N, size):
+    """The longest sequence without a running maximum, its rows' sums past fp32's range, and the
+    next one, with a maximum: with V the same for all keys O is V, up to the rounding of O and, with
+    a maximum, the 2^-8 of each bf16 weight. (A running maximum lags by up to 2^8, so its sums reach
+    2^8 N max|V|: 4e37 here, where values of 2e38 would pass fp32's 3.4e38 in any such kernel.
+    Without one they reach 2^72 N max|V|.)"""
+    dev = torch.device("cuda:0")
+    g = torch.Generator().manual_seed(31)
+    q, k = (torch.randn(1, 1, N, d, generator=g).to(dev) for _ in range(2))
+    row = (size * (1 + 0.5 * torch.rand(d, generator=g))).to(BF16).to(dev)
+    v = row.expand(1, 1, N, d).contiguous()
+    o, lse = fa.attention_forward((30 * q).to(BF16), k.to(BF16), v, causal=True, softcap=50.0)
+    torch.cuda.synchronize()
+    assert fa.fa_debug_status() == 0 and torch.isfinite(lse).all()
+    assert ((o.double() / row.double() - 1).abs() <= 2.0 ** -7).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_infinite_values_in_masked_places(d):
     """A value that is infinite, or not a number, reaches the rows that see its key alone."""
     dev = torch.device("cuda:0")
