@@ -221,8 +221,8 @@ fa_status_t fa_fwd_fp8(const void *q, const void *k, const void *v, float q_scal
  *            at most 80 ln 2 (55.45), no bias and N up to 98304, the fp32 sums behind O are of
  *            exp(score) V as it is, without the row's maximum taken off. Rows whose sums leave
  *            fp32's range (N max|V| above about 1e14 where scores lie at the cap; V below 1e-14
- *            where they all lie at its negative) are formed again, each for itself: right, but
- *            some hundred times slower.
+ *            where they all lie at its negative; values of V that are infinite or NaN) are
+ *            formed again, each for itself: right, but some hundred times slower.
  */
 typedef struct {
     const int *prefix_lengths;
